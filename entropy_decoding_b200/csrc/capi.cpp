@@ -3,6 +3,7 @@
 // codec.cpp (host) and decode.cu (device).
 #include <cuda_runtime_api.h>
 
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -13,6 +14,7 @@
 #include "gemm.h"
 #include "launch.h"
 #include "rans.h"
+#include "serve.h"
 
 struct df11_codebook {
     std::shared_ptr<df11::Codebook> cb;
@@ -80,6 +82,42 @@ df11_status gemm_jobs(const df11_gemm_matrix *mats, int n_mats, bool stand_ins, 
         jobs[i].x = stand_ins && !mats[i].x ? reinterpret_cast<const void *>(uintptr_t{256}) : mats[i].x;
         jobs[i].y = stand_ins && !mats[i].y ? reinterpret_cast<float *>(uintptr_t{256}) : mats[i].y;
     }
+    return DF11_OK;
+}
+
+bool misaligned(const void *p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+bool valid_page_size(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
+
+// Rows of n elements of a tensor whose rows are `stride` elements apart, each
+// starting on a 16-byte boundary.
+bool valid_rows(const void *p, uint64_t stride, uint64_t n, int elem_bytes) {
+    return p && !misaligned(p, 16) && stride >= n && stride < (uint64_t{1} << 40) && stride * elem_bytes % 16 == 0;
+}
+
+// need_pages: the call reads or writes the pages (a workspace query does not)
+df11_status check_cache(const df11_kv4_cache *c, bool need_pages) {
+    if (!c || c->n_heads < 1 || c->n_heads > 1024) return DF11_EINVAL;
+    if (!df11::kv4_supported(c->page_size, c->head_dim)) return DF11_EUNSUPPORTED;
+    if (!need_pages) return DF11_OK;
+    if (!c->pages || misaligned(c->pages, 16) || c->n_pages < 1 || c->n_pages >= (uint64_t{1} << 31)) return DF11_EINVAL;
+    if (!(c->k_scale > 0.0f) || !(c->v_scale > 0.0f) || std::isinf(c->k_scale) || std::isinf(c->v_scale))
+        return DF11_EINVAL;
+    return DF11_OK;
+}
+
+df11_status check_attention(const df11_kv4_cache *c, const df11_kv4_attention_args *a) {
+    if (a->n_reqs < 0 || a->n_tokens < 0 || a->max_q_len < 0 || a->n_q_heads < 1 || a->n_q_heads > 65535 ||
+        a->n_q_heads % c->n_heads)
+        return DF11_EINVAL;
+    return DF11_OK;
+}
+
+df11_status check_rope_side(const df11_rope_side &s, int head_dim, bool fp32) {
+    if (s.n_heads == 0) return DF11_OK;
+    const uint64_t row = static_cast<uint64_t>(s.n_heads) * head_dim;
+    if (!valid_rows(s.x, s.token_stride, row, fp32 ? 4 : 2) || !valid_rows(s.out, s.out_token_stride, row, 2) ||
+        misaligned(s.weight, 16))
+        return DF11_EINVAL;
     return DF11_OK;
 }
 
@@ -775,6 +813,104 @@ df11_status df11_rans_decode_launch_shape(const df11_rans_group *g, int *grid, i
     case df11::RansLaunch::kInvalid: return DF11_EINVAL;
     default: return DF11_ECUDA;
     }
+}
+
+// ---------------------------------------------------------------- serving a block
+
+df11_status df11_kv_extend(const df11_kv_extend_args *args, int *dev_err_flag, df11_stream stream) {
+    if (!args) return DF11_EINVAL;
+    const df11_kv_extend_args &a = *args;
+    if (a.n_reqs < 0 || a.max_pages < 0 || a.max_tokens < 0 || !valid_page_size(a.page_size)) return DF11_EINVAL;
+    if (!a.n_free || !a.free_pages || !a.q_start || !a.n_free_out) return DF11_EINVAL;
+    if (a.n_reqs && (!a.kv_lens || !a.new_lens || !a.kv_lens_out || (a.max_pages && !a.block_table))) return DF11_EINVAL;
+    if (a.max_tokens && (!a.slots || !a.positions)) return DF11_EINVAL;
+    if (misaligned(a.kv_lens, 4) || misaligned(a.new_lens, 4) || misaligned(a.free_pages, 4) || misaligned(a.n_free, 4) ||
+        misaligned(a.block_table, 4) || misaligned(a.kv_lens_out, 4) || misaligned(a.q_start, 4) ||
+        misaligned(a.slots, 8) || misaligned(a.positions, 4) || misaligned(a.n_free_out, 4))
+        return DF11_EINVAL;
+    return from_launch(df11::launch_kv_extend(a, dev_err_flag, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+df11_status df11_qk_norm_rope(const df11_qk_norm_rope_args *args, df11_stream stream) {
+    if (!args) return DF11_EINVAL;
+    const df11_qk_norm_rope_args &a = *args;
+    if (a.dtype != DF11_FP32 && a.dtype != DF11_BF16) return DF11_EINVAL;
+    if (a.n_tokens < 0 || a.q.n_heads < 0 || a.k.n_heads < 0 || a.q.n_heads > 65535 || a.k.n_heads > 65535 ||
+        a.interleaved < 0 || a.interleaved > 1 || !(a.eps >= 0.0f) || std::isinf(a.eps))
+        return DF11_EINVAL;
+    if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return DF11_EUNSUPPORTED;
+    if (a.rot_dim < 0 || a.rot_dim > a.head_dim || a.rot_dim % 8) return DF11_EINVAL;
+    if (a.rot_dim && (!a.positions || !a.inv_freq || misaligned(a.positions, 4) || misaligned(a.inv_freq, 8)))
+        return DF11_EINVAL;
+    for (const df11_rope_side *s : {&a.q, &a.k}) {
+        const df11_status st = check_rope_side(*s, a.head_dim, a.dtype == DF11_FP32);
+        if (st != DF11_OK) return st;
+    }
+    if (a.n_tokens == 0 || a.q.n_heads + a.k.n_heads == 0) return DF11_OK;
+    return from_launch(df11::launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+uint64_t df11_kv4_page_bytes(int page_size, int n_heads, int head_dim) {
+    if (!df11::kv4_supported(page_size, head_dim) || n_heads < 1 || n_heads > 1024) return 0;
+    return static_cast<uint64_t>(n_heads) * df11::kv4_block(page_size, head_dim).bytes;
+}
+
+df11_status df11_kv4_append(const df11_kv4_cache *cache, const void *k, uint64_t k_token_stride, const void *v,
+                            uint64_t v_token_stride, const int64_t *slots, int n_tokens, df11_dtype dtype,
+                            int *dev_err_flag, df11_stream stream) {
+    const df11_status st = check_cache(cache, true);
+    if (st != DF11_OK) return st;
+    if ((dtype != DF11_FP32 && dtype != DF11_BF16) || n_tokens < 0) return DF11_EINVAL;
+    if (n_tokens == 0) return DF11_OK;
+    const uint64_t row = static_cast<uint64_t>(cache->n_heads) * cache->head_dim;
+    const int eb = dtype == DF11_FP32 ? 4 : 2;
+    if (!valid_rows(k, k_token_stride, row, eb) || !valid_rows(v, v_token_stride, row, eb) || !slots ||
+        misaligned(slots, 8))
+        return DF11_EINVAL;
+    return from_launch(df11::launch_kv4_append(*cache, k, k_token_stride, v, v_token_stride, slots, n_tokens,
+                                               dtype == DF11_FP32, dev_err_flag,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+df11_status df11_kv4_gather(const df11_kv4_cache *cache, const int64_t *slots, int n_tokens, void *k_out, void *v_out,
+                            df11_dtype dtype, int *dev_err_flag, df11_stream stream) {
+    const df11_status st = check_cache(cache, true);
+    if (st != DF11_OK) return st;
+    if ((dtype != DF11_FP32 && dtype != DF11_BF16) || n_tokens < 0 || misaligned(k_out, 16) || misaligned(v_out, 16))
+        return DF11_EINVAL;
+    if (n_tokens == 0 || (!k_out && !v_out)) return DF11_OK;
+    if (!slots || misaligned(slots, 8)) return DF11_EINVAL;
+    return from_launch(df11::launch_kv4_gather(*cache, slots, n_tokens, k_out, v_out, dtype == DF11_FP32, dev_err_flag,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+uint64_t df11_kv4_attention_workspace_bytes(const df11_kv4_cache *cache, const df11_kv4_attention_args *args) {
+    uint64_t bytes = 0;
+    if (!args || check_cache(cache, false) != DF11_OK || check_attention(cache, args) != DF11_OK) return 0;
+    return df11::kv4_attention_workspace(*cache, *args, &bytes) == df11::LaunchStatus::kOk ? bytes : 0;
+}
+
+df11_status df11_kv4_attention(const df11_kv4_cache *cache, const df11_kv4_attention_args *args, int *dev_err_flag,
+                               df11_stream stream) {
+    if (!args) return DF11_EINVAL;
+    df11_status st = check_cache(cache, true);
+    if (st == DF11_OK) st = check_attention(cache, args);
+    if (st != DF11_OK) return st;
+    const df11_kv4_attention_args &a = *args;
+    if (a.causal < 0 || a.causal > 1 || a.window < 0 || (a.window && !a.causal) || !std::isfinite(a.scale) ||
+        a.max_pages < 0)
+        return DF11_EINVAL;
+    if (a.n_reqs == 0 || a.n_tokens == 0 || a.max_q_len == 0) return DF11_OK;
+    const uint64_t row = static_cast<uint64_t>(a.n_q_heads) * cache->head_dim;
+    if (!valid_rows(a.q, a.q_token_stride, row, 2) || !valid_rows(a.o, a.o_token_stride, row, 2) || !a.q_start ||
+        !a.kv_lens || (a.max_pages && !a.block_table) || misaligned(a.q_start, 4) || misaligned(a.kv_lens, 4) ||
+        misaligned(a.block_table, 4) || misaligned(a.lse, 4) || !a.workspace || misaligned(a.workspace, 16))
+        return DF11_EINVAL;
+    uint64_t need = 0;
+    const df11::LaunchStatus ls = df11::kv4_attention_workspace(*cache, a, &need);
+    if (ls != df11::LaunchStatus::kOk) return from_launch(ls);
+    if (a.workspace_bytes < need) return DF11_ENOMEM;
+    return from_launch(df11::launch_kv4_attention(*cache, a, dev_err_flag, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,268 @@
+// serve.cu -- what a decode step does around the fused GEMMs of a block's
+// attention, short of the cache itself: the step's pages, slots and positions
+// from the requests' lengths, and the norm and rotation of queries and keys.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "check.cuh"
+#include "df11.h"
+#include "serve.h"
+
+namespace df11 {
+namespace {
+
+__device__ __forceinline__ void flag(int *err, uint32_t bits) {
+    if (err && bits) atomicOr(err, static_cast<int>(bits));
+}
+
+// ------------------------------------------------------------------ pages, slots, positions
+
+// One launch, a thread per row (new token).  Every CTA scans the requests'
+// row and page counts itself, up to the requests its rows belong to: the
+// lengths are a few KB in L2, and a second launch or a wait between CTAs would
+// cost more than reading them again.  Sums are 64-bit, so no length overflows
+// them.  A row finds its request by bisection among the scanned starts; the
+// row that starts a page is the one that writes the page into the block table,
+// and every row computes its page's id from the free stack itself, so no
+// thread reads what another writes.
+constexpr int kExtendThreads = 512;
+
+__device__ __forceinline__ int64_t warp_incl(int64_t v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+
+__global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const df11_kv_extend_args A, int shift, int *err) {
+    __shared__ int64_t s_row[kExtendThreads], s_page[kExtendThreads];
+    __shared__ int32_t s_kv[kExtendThreads];
+    __shared__ int64_t s_sum[2][kExtendThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool first = blockIdx.x == 0;
+    const int64_t t_end = (static_cast<int64_t>(blockIdx.x) + 1) * kExtendThreads, t = t_end - kExtendThreads + tid;
+    const int32_t mask = A.page_size - 1;
+    const int64_t n_free = max(*A.n_free, 0);
+    uint32_t bad = 0;
+    int64_t rows = 0, pages = 0;  // of the requests before this tile
+    for (int base = 0; base < A.n_reqs && (first || rows < t_end); base += kExtendThreads) {
+        const int r = base + tid, cnt = min(kExtendThreads, A.n_reqs - base);
+        int32_t kv = 0, nw = 0;
+        if (r < A.n_reqs) {
+            kv = A.kv_lens[r];
+            nw = A.new_lens[r];
+            if (kv < 0 || nw < 0) bad |= DF11_DEV_ERR_AUX;
+            kv = max(kv, 0);
+            nw = max(nw, 0);
+        }
+        const int64_t len = static_cast<int64_t>(kv) + nw;
+        const int64_t np = ((len + mask) >> shift) - ((static_cast<int64_t>(kv) + mask) >> shift);
+        int64_t ri = warp_incl(nw, lane), pi = warp_incl(np, lane);
+        if (lane == 31) {
+            s_sum[0][warp] = ri;
+            s_sum[1][warp] = pi;
+        }
+        __syncthreads();
+        int64_t all_rows = 0, all_pages = 0;
+#pragma unroll
+        for (int w = 0; w < kExtendThreads / 32; ++w) {
+            if (w == warp) {
+                ri += all_rows;
+                pi += all_pages;
+            }
+            all_rows += s_sum[0][w];
+            all_pages += s_sum[1][w];
+        }
+        const int64_t row0 = rows + ri - nw;
+        s_row[tid] = row0;
+        s_page[tid] = pages + pi - np;
+        s_kv[tid] = kv;
+        if (first && r < A.n_reqs) {
+            A.kv_lens_out[r] = static_cast<int32_t>(min(len, static_cast<int64_t>(INT32_MAX)));
+            A.q_start[r] = static_cast<int32_t>(min(row0, static_cast<int64_t>(A.max_tokens)));
+            if (len > (static_cast<int64_t>(A.max_pages) << shift)) bad |= DF11_DEV_ERR_PAGES;
+        }
+        __syncthreads();
+        if (t >= rows && t < rows + all_rows && t < A.max_tokens) {
+            int i = 0;  // the last request that starts at or before t: the one with rows there
+#pragma unroll
+            for (int step = kExtendThreads / 2; step; step >>= 1)
+                if (i + step < cnt && s_row[i + step] <= t) i += step;
+            const int64_t pos = s_kv[i] + (t - s_row[i]);
+            const int64_t pg = pos >> shift;
+            int32_t id = -1;
+            if (pg < A.max_pages) {
+                int32_t *entry = A.block_table + static_cast<int64_t>(base + i) * A.max_pages + pg;
+                const int64_t held = (static_cast<int64_t>(s_kv[i]) + mask) >> shift;
+                if (pg < held) {
+                    id = *entry;
+                } else {
+                    const int64_t taken = s_page[i] + pg - held;
+                    if (taken < n_free) id = A.free_pages[n_free - 1 - taken];
+                    if ((pos & mask) == 0) *entry = id;
+                }
+            }
+            if (id < 0) bad |= DF11_DEV_ERR_PAGES;
+            A.slots[t] = id < 0 ? -1 : (static_cast<int64_t>(id) << shift) + (pos & mask);
+            A.positions[t] = static_cast<int32_t>(min(pos, static_cast<int64_t>(INT32_MAX)));
+        }
+        rows += all_rows;
+        pages += all_pages;
+        __syncthreads();
+    }
+    if (t >= rows && t < A.max_tokens) {  // padding
+        A.slots[t] = -1;
+        A.positions[t] = 0;
+    }
+    if (first && tid == 0) {
+        A.q_start[A.n_reqs] = static_cast<int32_t>(min(rows, static_cast<int64_t>(A.max_tokens)));
+        *A.n_free_out = static_cast<int32_t>(max(n_free - pages, static_cast<int64_t>(0)));
+        if (rows > A.max_tokens) bad |= DF11_DEV_ERR_AUX;
+        if (pages > n_free) bad |= DF11_DEV_ERR_PAGES;
+    }
+    flag(err, bad);
+}
+
+// ------------------------------------------------------------------ norm and rotation
+
+// head_dim / 8 lanes hold a head, 8 elements (4 pairs) each; a thread keeps
+// its 4 pairs' sines and cosines of one token and walks over that token's
+// heads, so the 64-bit angle and the sincos are paid once per token.  The
+// pass reads each element once and writes it once; nothing else goes to
+// memory.
+constexpr int kRopeThreads = 256;
+
+template <bool FP32>
+__device__ __forceinline__ void load4(const void *p, int64_t i, float *v) {
+    if constexpr (FP32) {
+        const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    } else {
+        const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+        v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void store4(void *p, int64_t i, const float *v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    uint2 o;
+    o.x = *reinterpret_cast<const uint32_t *>(&a);
+    o.y = *reinterpret_cast<const uint32_t *>(&b);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = o;
+}
+
+template <bool FP32, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const df11_qk_norm_rope_args A) {
+    constexpr int L = D / 8;                     // lanes of a head
+    constexpr int kHeads = kRopeThreads / L;     // heads the CTA holds at a time
+    const int64_t t = blockIdx.x;
+    const int j = threadIdx.x % L, half = A.rot_dim / 2;
+    // the thread's elements: 4 at oa, 4 at ob.  Halves layout: elements 4j ..
+    // of both halves while those are rotated, else 8 consecutive ones
+    // (rot_dim is a multiple of 8, so the two meet at element 8j = rot_dim)
+    const bool rotated = 4 * j < half;
+    const bool split = rotated && !INTER;
+    const int oa = split ? 4 * j : 8 * j, ob = split ? 4 * j + half : 8 * j + 4;
+    float cs[4], sn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = 1.0f, sn[i] = 0.0f;
+    if (rotated) {
+        const double pos = A.positions[t];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // in half turns, reduced to [-1, 1] in 64 bits: what 32 bits then
+            // round is the remainder, however far the position
+            double x = pos * A.inv_freq[4 * j + i] * 0.31830988618379067154;
+            x -= 2.0 * rint(0.5 * x);
+            sincospif(static_cast<float>(x), &sn[i], &cs[i]);
+        }
+    }
+    float w[2][8];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const void *wp = s ? A.k.weight : A.q.weight;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[s][i] = 1.0f;
+        if (wp) {
+            load4<false>(wp, oa, w[s]);
+            load4<false>(wp, ob, w[s] + 4);
+        }
+    }
+    const uint32_t group = (L == 32 ? 0xFFFFFFFFu : (1u << (L % 32)) - 1u) << (threadIdx.x & 31 & ~(L - 1));
+    const int heads = A.q.n_heads + A.k.n_heads;
+    for (int h = blockIdx.y * kHeads + threadIdx.x / L; h < heads; h += gridDim.y * kHeads) {
+        const bool is_k = h >= A.q.n_heads;
+        const df11_rope_side &S = is_k ? A.k : A.q;
+        const int64_t hd = static_cast<int64_t>(is_k ? h - A.q.n_heads : h) * D;
+        float v[8];
+        const int64_t at = t * static_cast<int64_t>(S.token_stride) + hd;
+        load4<FP32>(S.x, at + oa, v);
+        load4<FP32>(S.x, at + ob, v + 4);
+        if (S.weight) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1)
+                ss += __shfl_xor_sync(group, ss, o);
+            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + A.eps);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * (is_k ? w[1][i] : w[0][i]);
+        }
+        if (rotated) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float &a = v[INTER ? 2 * i : i], &b = v[INTER ? 2 * i + 1 : i + 4];
+                const float ra = a * cs[i] - b * sn[i];
+                b = b * cs[i] + a * sn[i];
+                a = ra;
+            }
+        }
+        const int64_t to = t * static_cast<int64_t>(S.out_token_stride) + hd;
+        store4(S.out, to + oa, v);
+        store4(S.out, to + ob, v + 4);
+    }
+}
+
+template <int D>
+void launch_rope(const df11_qk_norm_rope_args &a, dim3 grid, cudaStream_t s) {
+    if (a.dtype == DF11_FP32)
+        a.interleaved ? qk_norm_rope_kernel<true, D, true><<<grid, kRopeThreads, 0, s>>>(a)
+                      : qk_norm_rope_kernel<true, D, false><<<grid, kRopeThreads, 0, s>>>(a);
+    else
+        a.interleaved ? qk_norm_rope_kernel<false, D, true><<<grid, kRopeThreads, 0, s>>>(a)
+                      : qk_norm_rope_kernel<false, D, false><<<grid, kRopeThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
+LaunchStatus launch_kv_extend(const df11_kv_extend_args &a, int *err, cudaStream_t s) {
+    int shift = 0;
+    while ((1 << shift) < a.page_size) ++shift;
+    const unsigned grid = a.max_tokens > 0 ? (a.max_tokens + kExtendThreads - 1) / kExtendThreads : 1;
+    kv_extend_kernel<<<grid, kExtendThreads, 0, s>>>(a, shift, err);
+    return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;
+}
+
+LaunchStatus launch_qk_norm_rope(const df11_qk_norm_rope_args &a, cudaStream_t s) {
+    const int heads = a.q.n_heads + a.k.n_heads, per = kRopeThreads / (a.head_dim / 8);
+    // few tokens: a CTA per token and group of heads, so that every element
+    // has its own thread at once; many: one CTA per token
+    const int groups = (heads + per - 1) / per;
+    const dim3 grid(a.n_tokens, static_cast<int64_t>(a.n_tokens) * groups <= 4 * 148 ? groups : 1);
+    switch (a.head_dim) {
+        case 64: launch_rope<64>(a, grid, s); break;
+        case 128: launch_rope<128>(a, grid, s); break;
+        case 256: launch_rope<256>(a, grid, s); break;
+        default: return LaunchStatus::kUnsupported;
+    }
+    return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;
+}
+
+}  // namespace df11

@@ -39,9 +39,11 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 DF11_OK, DF11_EINVAL, DF11_ENOMEM, DF11_ECUDA, DF11_ECORRUPT, DF11_EUNSUPPORTED = range(6)
-DF11_BF16, DF11_FP8_E4M3 = 0, 1
+DF11_BF16, DF11_FP8_E4M3, DF11_FP32 = 0, 1, 2
 DTYPES = {"bf16": DF11_BF16, "e4m3": DF11_FP8_E4M3}
+ACTIVATIONS = {"bf16": DF11_BF16, "fp32": DF11_FP32}  # of the serving operators
 DEV_ERR_SPAN, DEV_ERR_CODE, DEV_ERR_AUX, DEV_ERR_TIMEOUT, DEV_ERR_BOUNDS = 1, 2, 4, 8, 16
+DEV_ERR_PAGES = 32
 
 
 class Df11Error(RuntimeError):
@@ -84,6 +86,42 @@ class DecodeOpts(ctypes.Structure):
 class GemmMatrix(ctypes.Structure):
     _fields_ = [("weights", ctypes.c_void_p), ("k", ctypes.c_uint64), ("n", ctypes.c_uint64), ("x", ctypes.c_void_p),
                 ("y", ctypes.c_void_p)]
+
+
+class KvExtendArgs(ctypes.Structure):
+    _fields_ = [("kv_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("n_reqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("page_size", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("kv_lens_out", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("n_free_out", ctypes.c_void_p)]
+
+
+class RopeSide(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("token_stride", ctypes.c_uint64), ("weight", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_token_stride", ctypes.c_uint64), ("n_heads", ctypes.c_int32)]
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("q", RopeSide), ("k", RopeSide), ("n_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p)]
+
+
+class Kv4Cache(ctypes.Structure):
+    """A paged 4-bit key/value cache: (pages device pointer, n_pages, page_size,
+    n_heads, head_dim, k_scale, v_scale).  The memory stays the caller's."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_uint64), ("page_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
+class Kv4AttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_uint64), ("o", ctypes.c_void_p),
+                ("o_token_stride", ctypes.c_uint64), ("lse", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("n_reqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
 
 
 GEMM_TILE_N, GEMM_TILE_K, GEMM_MAX_MATS, GEMM_MAX_BATCH = 128, 64, 8, 64
@@ -148,6 +186,13 @@ _SIGS = {
     "df11_rans_group_deserialize": ([_P, _U64, _PP], _S),
     "df11_rans_group_upload": ([_P, _P, _U64, _P], _S),
     "df11_rans_decode": ([_P, _PP, _P, _P], _S),
+    "df11_kv_extend": ([ctypes.POINTER(KvExtendArgs), _P, _P], _S),
+    "df11_qk_norm_rope": ([ctypes.POINTER(QkNormRopeArgs), _P], _S),
+    "df11_kv4_page_bytes": ([_I, _I, _I], _U64),
+    "df11_kv4_append": ([ctypes.POINTER(Kv4Cache), _P, _U64, _P, _U64, _P, _I, _I, _P, _P], _S),
+    "df11_kv4_gather": ([ctypes.POINTER(Kv4Cache), _P, _I, _P, _P, _I, _P, _P], _S),
+    "df11_kv4_attention_workspace_bytes": ([ctypes.POINTER(Kv4Cache), ctypes.POINTER(Kv4AttentionArgs)], _U64),
+    "df11_kv4_attention": ([ctypes.POINTER(Kv4Cache), ctypes.POINTER(Kv4AttentionArgs), _P, _P], _S),
     "df11_rans_decode_launch_shape": ([_P, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_I)], _S),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -483,6 +528,70 @@ def df11_decode_gemm_launch_shape(mats, m: int):
     _check(_lib.df11_decode_gemm_launch_shape(_gemm_array(mats), len(mats), m, ctypes.byref(g), ctypes.byref(b),
                                               ctypes.byref(s)), "df11_decode_gemm_launch_shape")
     return g.value, b.value, s.value
+
+
+# ----------------------------------------------------------------- serving a block
+
+def df11_kv_extend(kv_lens_ptr: int, new_lens_ptr: int, n_reqs: int, free_pages_ptr: int, n_free_ptr: int,
+                   block_table_ptr: int, max_pages: int, page_size: int, kv_lens_out_ptr: int, q_start_ptr: int,
+                   slots_ptr: int, positions_ptr: int, max_tokens: int, n_free_out_ptr: int,
+                   err_ptr: int | None = None, stream: int = 0):
+    """One step's pages, block tables, slots and positions from the requests' lengths, all on the device."""
+    a = KvExtendArgs(kv_lens_ptr or None, new_lens_ptr or None, n_reqs, max_pages, free_pages_ptr or None,
+                     n_free_ptr or None, block_table_ptr or None, page_size, max_tokens, kv_lens_out_ptr or None,
+                     q_start_ptr or None, slots_ptr or None, positions_ptr or None, n_free_out_ptr or None)
+    _check(_lib.df11_kv_extend(a, err_ptr or None, stream or None), "df11_kv_extend")
+
+
+def _rope_side(side) -> RopeSide:
+    if side is None:
+        return RopeSide()
+    x, stride, weight, out, out_stride, n_heads = side
+    return RopeSide(x or None, stride, weight or None, out or None, out_stride, n_heads)
+
+
+def df11_qk_norm_rope(q, k, n_tokens: int, head_dim: int, positions_ptr: int, inv_freq_ptr: int, rot_dim: int,
+                      interleaved: bool = False, eps: float = 1e-6, dtype: str = "fp32", stream: int = 0):
+    """q, k: (x pointer, token stride, norm weight pointer or 0, out pointer, out token stride, heads), strides in
+    elements, or None: that side is absent.  dtype: of x, "fp32" or "bf16"; out is BF16."""
+    a = QkNormRopeArgs(_rope_side(q), _rope_side(k), n_tokens, head_dim, rot_dim, int(interleaved), ACTIVATIONS[dtype],
+                       eps, positions_ptr or None, inv_freq_ptr or None)
+    _check(_lib.df11_qk_norm_rope(a, stream or None), "df11_qk_norm_rope")
+
+
+def df11_kv4_page_bytes(page_size: int, n_heads: int, head_dim: int) -> int:
+    """Bytes of one page of the 4-bit cache (all heads); 0 for a size that is not supported."""
+    return int(_lib.df11_kv4_page_bytes(page_size, n_heads, head_dim))
+
+
+def df11_kv4_append(cache: Kv4Cache, k_ptr: int, k_token_stride: int, v_ptr: int, v_token_stride: int, slots_ptr: int,
+                    n_tokens: int, dtype: str = "bf16", err_ptr: int | None = None, stream: int = 0):
+    _check(_lib.df11_kv4_append(cache, k_ptr or None, k_token_stride, v_ptr or None, v_token_stride, slots_ptr or None,
+                                n_tokens, ACTIVATIONS[dtype], err_ptr or None, stream or None), "df11_kv4_append")
+
+
+def df11_kv4_gather(cache: Kv4Cache, slots_ptr: int, n_tokens: int, k_out_ptr: int, v_out_ptr: int,
+                    dtype: str = "bf16", err_ptr: int | None = None, stream: int = 0):
+    _check(_lib.df11_kv4_gather(cache, slots_ptr or None, n_tokens, k_out_ptr or None, v_out_ptr or None,
+                                ACTIVATIONS[dtype], err_ptr or None, stream or None), "df11_kv4_gather")
+
+
+def df11_kv4_attention_workspace_bytes(cache: Kv4Cache, n_q_heads: int, n_reqs: int, n_tokens: int,
+                                       max_q_len: int) -> int:
+    """Workspace of df11_kv4_attention for these sizes; 0 when one is invalid.  Zero it once before its first use."""
+    a = Kv4AttentionArgs(n_reqs=n_reqs, n_tokens=n_tokens, n_q_heads=n_q_heads, max_q_len=max_q_len)
+    return int(_lib.df11_kv4_attention_workspace_bytes(cache, a))
+
+
+def df11_kv4_attention(cache: Kv4Cache, q_ptr: int, q_token_stride: int, o_ptr: int, o_token_stride: int,
+                       n_q_heads: int, q_start_ptr: int, kv_lens_ptr: int, block_table_ptr: int, n_reqs: int,
+                       max_pages: int, n_tokens: int, max_q_len: int, scale: float, workspace_ptr: int,
+                       workspace_bytes: int, causal: bool = True, window: int = 0, lse_ptr: int | None = None,
+                       err_ptr: int | None = None, stream: int = 0):
+    a = Kv4AttentionArgs(q_ptr or None, q_token_stride, o_ptr or None, o_token_stride, lse_ptr or None,
+                         q_start_ptr or None, kv_lens_ptr or None, block_table_ptr or None, n_reqs, max_pages, n_tokens,
+                         n_q_heads, max_q_len, int(causal), window, scale, workspace_ptr or None, workspace_bytes)
+    _check(_lib.df11_kv4_attention(cache, a, err_ptr or None, stream or None), "df11_kv4_attention")
 
 
 # ----------------------------------------------------------------- torch-side helpers (device memory only)

@@ -51,7 +51,8 @@ typedef enum {
 
 typedef enum {
     DF11_BF16 = 0,      /* 16-bit words: sign | 8-bit exponent | 7-bit mantissa */
-    DF11_FP8_E4M3 = 1   /* bytes: sign | 4-bit exponent | 3-bit mantissa */
+    DF11_FP8_E4M3 = 1,  /* bytes: sign | 4-bit exponent | 3-bit mantissa */
+    DF11_FP32 = 2       /* 32-bit floats: activations of the serving operators only, never coded */
 } df11_dtype;
 
 /* Bits the decode kernel ORs into the caller's device error word.  Any
@@ -65,6 +66,8 @@ typedef enum {
 #define DF11_DEV_ERR_BOUNDS 16u  /* bounds-checked debug build only (libdf11_check.so, built with
                                     -DDF11_CHECK=1): a shared- or global-memory access fell outside
                                     its buffer or section and was skipped; never set by libdf11.so */
+#define DF11_DEV_ERR_PAGES 32u   /* serving operators: a page, slot or block-table entry out of range, or no
+                                    free page left; what it named was skipped */
 
 /* Same type as cudaStream_t; pass 0 for the legacy default stream. */
 typedef struct CUstream_st *df11_stream;
@@ -623,6 +626,187 @@ df11_status df11_rans_decode(const df11_rans_group *g, void *const *dst_dev, int
 /* Grid, threads per CTA and dynamic shared memory of that launch (any output
  * may be NULL; the group must be bound). */
 df11_status df11_rans_decode_launch_shape(const df11_rans_group *g, int *grid, int *block, int *smem_bytes);
+
+/* ---------------------------------------------------------------------
+ * Serving a block: positions, norms and the 4-bit key/value cache
+ *
+ * What weights held compressed leave free goes to the key/value cache
+ * (DFloat11 Abstract: longer generations in the same GPU memory).  These
+ * operators stand between the fused GEMMs of a block's query, key and value
+ * matrices and that of its output matrix, in this order per step:
+ *   df11_kv_extend      the step's pages, slots and positions
+ *   df11_decode_gemm    q, k, v = x Wq, x Wk, x Wv (FP32)
+ *   df11_qk_norm_rope   norm and rotation of q and k (FP32 -> BF16)
+ *   df11_kv4_append     k, v into the cache, 4 bits an element
+ *   df11_kv4_attention  o = softmax(q k^T) v, the cache decoded on the way
+ *                       into the tensor cores (BF16: x of the next GEMM)
+ * All are asynchronous on `stream`, allocate nothing, never synchronise, and
+ * can be captured into a graph: lengths are read on the device.  Requests
+ * are "ragged": request r's tokens are rows q_start[r] .. q_start[r + 1] - 1.
+ * dev_err_flag (nullable) as in df11_decode.  Buffers may not overlap unless
+ * stated.  These are lossy (the cache) or ordinary floating-point operators;
+ * the weights' lossless path does not pass through them.
+ * ------------------------------------------------------------------ */
+
+/* Arguments of df11_kv_extend; every pointer is device memory. */
+typedef struct {
+    const int32_t *kv_lens;    /* n_reqs: tokens of each request already in the cache */
+    const int32_t *new_lens;   /* n_reqs: tokens this step adds (0 allowed) */
+    int32_t n_reqs;
+    int32_t max_pages;         /* entries of a block_table row */
+    const int32_t *free_pages; /* stack of free page ids, the top at *n_free - 1 */
+    const int32_t *n_free;
+    int32_t *block_table;      /* n_reqs x max_pages, in and out: entries of the pages held stay, entries of
+                                  the pages taken are written, the rest is left as it was */
+    int32_t page_size;         /* tokens per page: 16, 32, 64 or 128 */
+    int32_t max_tokens;        /* entries of slots and positions */
+    int32_t *kv_lens_out;      /* n_reqs: kv_lens + new_lens */
+    int32_t *q_start;          /* n_reqs + 1: first row of each request, the last entry the row count */
+    int64_t *slots;            /* max_tokens: page id * page_size + place in the page of each row; -1 in the
+                                  rows behind the last request (padding) and where there is no page */
+    int32_t *positions;        /* max_tokens: the row's position in its request; 0 in padding */
+    int32_t *n_free_out;       /* *n_free less the pages taken */
+} df11_kv_extend_args;
+
+/* Pages, block tables, slots and positions of one step, from the requests'
+ * lengths, in ONE launch.  Request by request in order, and within a request
+ * in order of position, each page that a new token starts is the top of the
+ * free stack.  free_pages and *n_free are only read: the same call again
+ * gives the same result, and the next step passes kv_lens_out and n_free_out
+ * as its inputs.
+ * DF11_DEV_ERR_PAGES: the free stack ran out, a row is longer than
+ * max_pages, or a held page's entry is negative (those rows get slot -1).
+ * DF11_DEV_ERR_AUX: a negative length (taken as 0), or more rows than
+ * max_tokens (q_start is cut there, the rows past it have no slot).
+ * Errors: DF11_EINVAL (NULL or misaligned pointer, sizes), DF11_ECUDA. */
+df11_status df11_kv_extend(const df11_kv_extend_args *args, int *dev_err_flag, df11_stream stream);
+
+/* One side (queries or keys) of df11_qk_norm_rope: element (t, h, d) of x at
+ * t * token_stride + h * head_dim + d, of out at t * out_token_stride +
+ * h * head_dim + d. */
+typedef struct {
+    const void *x;             /* device, DF11_FP32 or DF11_BF16, 16-byte aligned rows */
+    uint64_t token_stride;     /* elements, at least n_heads * head_dim */
+    const void *weight;        /* device, head_dim BF16 norm weights, or NULL: no norm */
+    void *out;                 /* device, BF16, 16-byte aligned rows; with BF16 x it may be x itself */
+    uint64_t out_token_stride;
+    int32_t n_heads;           /* 0: this side is absent */
+} df11_rope_side;
+
+typedef struct {
+    df11_rope_side q, k;
+    int32_t n_tokens;
+    int32_t head_dim;          /* 64, 128 or 256 */
+    int32_t rot_dim;           /* elements rotated, from the first: a multiple of 8, 0..head_dim */
+    int32_t interleaved;       /* pairs (2i, 2i + 1) when 1, (i, i + rot_dim / 2) when 0 */
+    int32_t dtype;             /* of x: DF11_FP32 or DF11_BF16 */
+    float eps;                 /* >= 0 */
+    const int32_t *positions;  /* device, n_tokens */
+    const double *inv_freq;    /* device, rot_dim / 2: radians per position of each pair (any scaling of the
+                                  frequencies is the caller's) */
+} df11_qk_norm_rope_args;
+
+/* Norm of every head and rotation by the token's position, one pass over the
+ * rows of both sides, one launch: y = x / sqrt(mean(x^2) + eps) * weight over
+ * a head's head_dim elements (left out when weight is NULL), then each pair
+ * (a, b) -> (a cos - b sin, b cos + a sin), the angle position * inv_freq in
+ * 64 bits; FP32 throughout, rounded to BF16 once.
+ * Errors: DF11_EINVAL (NULL or misaligned pointer or stride, sizes, eps),
+ * DF11_EUNSUPPORTED (head_dim), DF11_ECUDA. */
+df11_status df11_qk_norm_rope(const df11_qk_norm_rope_args *args, df11_stream stream);
+
+/* The paged 4-bit key/value cache of one layer.  16 consecutive elements of
+ * a head share one scale s in FP8 E4M3; an element is an E2M1 level (0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives) and stands for level * s * k_scale
+ * (v_scale for values): 4.5 bits an element.  The block of one head in a page
+ * is page_size * head_dim * 9 / 8 contiguous bytes, page p, head h at
+ * pages + (p * n_heads + h) * that:
+ *   K codes   row t: head_dim / 2 bytes, element 2i in the low nibble of byte i
+ *   K scales  row t: head_dim / 16 bytes
+ *   V codes   [page_size / 4][head_dim / 16][4][8]: 8 bytes of token 4a + c,
+ *             elements 16b .. 16b + 15, at [a][b][c]
+ *   V scales  [head_dim / 16][page_size]
+ * A byte belongs to one token, so tokens are written without reading. */
+typedef struct {
+    void *pages;               /* device, n_pages * df11_kv4_page_bytes, 16-byte aligned */
+    uint64_t n_pages;          /* 1 .. 2^31 - 1 */
+    int32_t page_size;         /* 16, 32, 64 or 128 tokens */
+    int32_t n_heads;           /* key/value heads, 1 .. 1024 */
+    int32_t head_dim;          /* 64 or 128 */
+    float k_scale, v_scale;    /* positive, finite */
+} df11_kv4_cache;
+
+/* Bytes of one page (all heads); 0 for a size that is not supported. */
+uint64_t df11_kv4_page_bytes(int page_size, int n_heads, int head_dim);
+
+/* Writes token t's keys and values (k and v: element (t, h, d) at
+ * t * stride + h * head_dim + d, strides in elements, rows 16-byte aligned,
+ * dtype DF11_BF16 or DF11_FP32, FP32 rounded to BF16 first) into slot
+ * slots[t]; a negative slot is skipped, other slots are not touched.  Per 16
+ * elements: s = E4M3(min((max |x| / 6) / scale, 448)), level = E2M1(x / (s *
+ * scale)), saturating at 6, in FP32 arithmetic, both to nearest, ties to
+ * even; s = 0 gives levels 0.  An infinite element makes s 448; a NaN does
+ * not count for s and is held as +6 (0 where s is 0).  The slots of one call
+ * are distinct; of a slot named twice only that slot's contents are
+ * undefined.  DF11_DEV_ERR_PAGES: a slot past the cache (skipped).  Errors:
+ * DF11_EINVAL, DF11_EUNSUPPORTED (head_dim or page_size), DF11_ECUDA. */
+df11_status df11_kv4_append(const df11_kv4_cache *cache, const void *k, uint64_t k_token_stride, const void *v,
+                            uint64_t v_token_stride, const int64_t *slots, int n_tokens, df11_dtype dtype,
+                            int *dev_err_flag, df11_stream stream);
+
+/* Reads tokens back: the value each element stands for, rounded to dtype
+ * (DF11_BF16 or DF11_FP32), to k_out and v_out (n_tokens x n_heads x
+ * head_dim, contiguous, 16-byte aligned; either may be NULL).  Rows of a
+ * negative slot are left as they were.  Errors as df11_kv4_append. */
+df11_status df11_kv4_gather(const df11_kv4_cache *cache, const int64_t *slots, int n_tokens, void *k_out, void *v_out,
+                            df11_dtype dtype, int *dev_err_flag, df11_stream stream);
+
+/* Arguments of df11_kv4_attention; every pointer is device memory. */
+typedef struct {
+    const void *q;              /* BF16, element (t, h, d) at t * q_token_stride + h * head_dim + d, rows
+                                   16-byte aligned */
+    uint64_t q_token_stride;    /* elements */
+    void *o;                    /* BF16, laid out as q with o_token_stride */
+    uint64_t o_token_stride;
+    float *lse;                 /* n_tokens x n_q_heads, or NULL: log(sum exp) of each row's scaled scores */
+    const int32_t *q_start;     /* n_reqs + 1: rows of each request, not descending */
+    const int32_t *kv_lens;     /* n_reqs: keys of each request, its new tokens among them */
+    const int32_t *block_table; /* n_reqs x max_pages */
+    int32_t n_reqs, max_pages;
+    int32_t n_tokens;           /* rows of q and o */
+    int32_t n_q_heads;          /* a multiple of the cache's n_heads; query head h reads cache head
+                                   h / (n_q_heads / n_heads) */
+    int32_t max_q_len;          /* upper bound on a request's rows */
+    int32_t causal;             /* 1: row i of n sees keys 0 .. kv_len - n + i; 0: every key */
+    int32_t window;             /* with causal: only the last `window` of those; 0 = all */
+    float scale;                /* of the scores, finite */
+    void *workspace;            /* df11_kv4_attention_workspace_bytes, 16-byte aligned; all zero before its
+                                   first use, after which every call leaves what the next one needs.
+                                   Calls that may run at the same time need one each */
+    uint64_t workspace_bytes;
+} df11_kv4_attention_args;
+
+/* Workspace of that call on the current device for the cache's shape and the
+ * args' n_q_heads, n_reqs, n_tokens and max_q_len (pointers are not read); 0
+ * when a value is invalid. */
+uint64_t df11_kv4_attention_workspace_bytes(const df11_kv4_cache *cache, const df11_kv4_attention_args *args);
+
+/* o = softmax(scale * q k^T + mask) v over each request's keys in the cache,
+ * decoded on chip.  Softmax statistics and sums in FP32; the products run on
+ * the tensor cores in FP16 with FP32 sums (keys and values are exact in FP16,
+ * each row of q is scaled by a power of two into FP16's range, probabilities
+ * are rounded to FP16).  A row that sees no key gets o = 0 and lse = -inf.
+ * Rows behind q_start[n_reqs] are left as they were.  What the pages hold
+ * past a request's kv_len never reaches an output.  The result does not
+ * depend on timing: calls with equal arguments give equal bits.
+ * DF11_DEV_ERR_PAGES: a block-table entry out of range, or kv_len past
+ * max_pages * page_size (those keys are left out).  DF11_DEV_ERR_AUX:
+ * q_start descending or past n_tokens, or a request longer than max_q_len
+ * (those rows are not written).
+ * Errors: DF11_EINVAL, DF11_EUNSUPPORTED (head_dim or page_size), DF11_ENOMEM
+ * (workspace too small), DF11_ECUDA. */
+df11_status df11_kv4_attention(const df11_kv4_cache *cache, const df11_kv4_attention_args *args, int *dev_err_flag,
+                               df11_stream stream);
 
 #ifdef __cplusplus
 }
