@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -10,6 +11,7 @@
 #include "df11.h"
 #include "kv4.cuh"
 #include "serve.h"
+#include "tcgen05.cuh"
 #include "walk.cuh"
 
 namespace df11 {
@@ -26,12 +28,6 @@ struct AttnParams {
     uint64_t wait_ns;   // limit of each wait for a copy
     uint32_t ws_parts;  // workspace, in floats: counters before, partial results from here
 };
-
-__device__ __forceinline__ void f16x2_to_f32(uint32_t v, float &lo, float &hi) {
-    asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(v));
-}
 
 // ------------------------------------------------------------------ few rows: keys shared out over the GPU
 
@@ -709,88 +705,564 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     report(P.err, __reduce_or_sync(0xFFFFFFFFu, err) * (lane == 0));
 }
 
-// A warp per row and query head, 4 warps of a CTA splitting the row's keys; a
-// lane holds D / 32 elements.
+// ------------------------------------------------------------------ many rows: tcgen05
+
+// A CTA takes 256 rows (token, query head of the group) of one request and
+// cache head, as two tiles of 128 that share every decoded key and value:
+//   * warps 0-3 and 4-7: softmax of a tile each, a thread per row: scores out
+//     of TMEM, probabilities (FP16) back into the same columns;
+//   * warps 8-11: the cache's codes to FP16 operand tiles of 128 keys in
+//     shared memory, K as rows of keys and V as rows of elements (transposed
+//     while it is decoded: two keys' codes become one byte, one conversion
+//     gives the pair, and a thread's 8 keys make a 16-byte chunk);
+//   * warp 12: the MMAs, S = Q K^T and O += P V with P taken from TMEM.  The
+//     tiles alternate, so the tensor cores work on one while the other's
+//     softmax runs.
+// TMEM holds both tiles' S (128 columns, P over them) and O.  O is rescaled
+// only when a row's maximum grew by more than 2^8: P then stays below 2^8 in
+// FP16, and most steps leave O alone.  Waits are bounded; one that gives up
+// sets a flag that ends the others.
+constexpr int kPrefillThreads = 512;
+constexpr int kPrefillTile = 128;  // rows of a tile, keys of a step
+constexpr float kLazy = 8.0f;      // log2 units a row's maximum may grow before O is rescaled
+
 template <int D>
-__global__ void __launch_bounds__(128) attention_rows_kernel(const AttnParams P) {
-    constexpr int E = D / 32;
-    __shared__ float s_m[4], s_l[4], s_o[4][D];
+struct PrefillShared {
+    static constexpr uint32_t kOperand = kPrefillTile * D * 2;
+    alignas(1024) uint8_t q[2][kOperand];
+    uint8_t k[2][kOperand], v[2][kOperand];
+    uint32_t ok[4][4];  // keys of a step that are there; the softmax may read a step's while the next two are decoded
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], end;
+    int32_t sums[kPrefillThreads / 32];
+    uint32_t tmem, abort;
+    int32_t req, pair;
+};
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in an operand tile whose
+// rows are 128 bytes in the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz_chunk(uint32_t row, uint32_t chunk) {
+    return row * 128u + ((chunk ^ (row & 7u)) << 4);
+}
+
+// Shared-memory matrix descriptor of such a tile (K-major, 8-row groups 1024 bytes apart).
+__device__ __forceinline__ uint64_t swz128_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (uint64_t{1} << 16) | (uint64_t{1024 >> 4} << 32) |
+           (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+template <class Shared>
+__device__ __forceinline__ bool prefill_wait_slow(uint64_t *bar, uint32_t parity, Shared &S, uint64_t limit_ns) {
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile uint32_t *>(&S.abort)) return false;
+        if (global_ns() - t0 > limit_ns) {
+            atomicExch(&S.abort, 1u);
+            return false;
+        }
+    }
+}
+
+template <class Shared>
+__device__ __forceinline__ bool prefill_wait(uint64_t *bar, uint32_t parity, Shared &S, uint64_t limit_ns) {
+    return mbar_try_wait(bar, parity) || prefill_wait_slow(bar, parity, S, limit_ns);
+}
+
+// What the CTA works on: rows [row0, rows) of a request, and per tile the key
+// steps [a0, a1) that its rows see, counted from key first * 128.
+struct PrefillWork {
+    int32_t req, q0, n, rows, row0, first, steps, a0[2], a1[2];
+    int64_t kv, begin, end;  // keys; the first and the last + 1 that any row can see
+};
+
+__device__ __forceinline__ int prefill_pairs(const AttnParams &P, int r) {
+    if (r >= P.a.n_reqs) return 0;
+    const int q0 = __ldg(P.a.q_start + r), q1 = __ldg(P.a.q_start + r + 1);
+    if (!rows_valid(P.a, q0, q1)) return 0;
+    const int64_t rows = static_cast<int64_t>(q1 - q0) * P.group;
+    return rows > kSplitMaxRows ? static_cast<int>((rows + 2 * kPrefillTile - 1) / (2 * kPrefillTile)) : 0;
+}
+
+// Keys [lo, hi) that row `row` of the request sees.
+__device__ __forceinline__ void prefill_row(const AttnParams &P, const PrefillWork &W, int row, int64_t &lo, int64_t &hi) {
+    const int64_t pos = W.kv - W.n + row / static_cast<int>(P.group);
+    hi = max(P.a.causal ? min(pos + 1, W.end) : W.end, static_cast<int64_t>(0));
+    lo = P.a.window ? min(max(pos + 1 - P.a.window, static_cast<int64_t>(0)), hi) : 0;
+}
+
+__device__ __forceinline__ PrefillWork prefill_work(const AttnParams &P, int req, int pair) {
+    PrefillWork W;
+    W.req = req;
+    W.q0 = __ldg(P.a.q_start + req);
+    W.n = __ldg(P.a.q_start + req + 1) - W.q0;
+    W.rows = W.n * static_cast<int>(P.group);
+    W.row0 = pair * 2 * kPrefillTile;
+    W.kv = max(__ldg(P.a.kv_lens + req), 0);
+    W.end = min(W.kv, static_cast<int64_t>(P.a.max_pages) << P.page_shift);
+    int64_t b[2], e[2], first = INT64_MAX, last = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int r0 = W.row0 + x * kPrefillTile, r1 = min(r0 + kPrefillTile, W.rows) - 1;
+        b[x] = e[x] = 0;
+        if (r0 <= r1) {
+            int64_t lo0, hi0, lo1, hi1;
+            prefill_row(P, W, r0, lo0, hi0);
+            prefill_row(P, W, r1, lo1, hi1);
+            if (x == 0) W.begin = lo0;
+            if (hi1 > 0) b[x] = lo0 / kPrefillTile, e[x] = (hi1 + kPrefillTile - 1) / kPrefillTile;
+        }
+        if (e[x] > b[x]) first = min(first, b[x]), last = max(last, e[x]);
+    }
+    if (last == 0) first = 0;
+    W.first = static_cast<int32_t>(first);
+    W.steps = static_cast<int32_t>(last - first);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        W.a0[x] = e[x] > b[x] ? static_cast<int32_t>(b[x] - first) : 0;
+        W.a1[x] = e[x] > b[x] ? static_cast<int32_t>(e[x] - first) : 0;
+    }
+    return W;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// The block-table entry of key `key`, or kNoPage where the page holds no key a row sees.
+__device__ __forceinline__ int64_t prefill_page(const AttnParams &P, const PrefillWork &W, int64_t key) {
+    if (key >= W.end || (((key >> P.page_shift) + 1) << P.page_shift) <= W.begin) return kNoPage;
+    return __ldg(P.a.block_table + static_cast<int64_t>(W.req) * P.a.max_pages + (key >> P.page_shift));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(const AttnParams P) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    PrefillShared<D> &S =
+        *reinterpret_cast<PrefillShared<D> *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
     const df11_kv4_attention_args &A = P.a;
-    const int t = blockIdx.x, hq = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t h = hq / P.group;
-    uint32_t bad = 0;
-    // the last request that starts at or before row t
-    int lo = 0, hi = A.n_reqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        (A.q_start[mid] <= t ? lo : hi) = mid;
-    }
-    const int q0 = A.q_start[lo], q1 = A.q_start[lo + 1];
-    if (t < q0 || t >= q1) return;
-    if (!rows_valid(A, q0, q1) || static_cast<int64_t>(q1 - q0) * P.group <= kSplitMaxRows) return;
-    int64_t kv = max(A.kv_lens[lo], 0);
-    const int64_t cap = static_cast<int64_t>(A.max_pages) << P.page_shift;
-    const int64_t pos = kv - (q1 - q0) + (t - q0);
-    int64_t j0 = 0, j1 = A.causal ? min(pos + 1, kv) : kv;
-    if (A.window) j0 = max(j0, pos + 1 - A.window);
-    j1 = min(j1, cap);
-    float q[E], o[E], m = -INFINITY, l = 0.0f;
-    const __nv_bfloat16 *qp =
-        static_cast<const __nv_bfloat16 *>(A.q) + t * static_cast<int64_t>(A.q_token_stride) + hq * D + lane * E;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int head = blockIdx.y, group = static_cast<int>(P.group);
+
+    // ---- this CTA's request and rows: pairs of tiles counted over the
+    // requests; the last rows first, which see the most keys
+    {
+        int all = 0, want = -1;
+        for (int pass = 0; pass < 2; ++pass) {
+            int base = 0;
+            for (int b = 0; b < A.n_reqs; b += kPrefillThreads) {
+                const int w = prefill_pairs(P, b + tid);
+                int incl = w;
 #pragma unroll
-    for (int i = 0; i < E; ++i) q[i] = __bfloat162float(qp[i]) * A.scale * P.k_scale, o[i] = 0.0f;
-    for (int64_t j = j0 + warp; j < j1; j += 4) {
-        const int32_t id = A.block_table[static_cast<int64_t>(lo) * A.max_pages + (j >> P.page_shift)];
-        if (id < 0 || static_cast<uint64_t>(id) >= P.n_pages) {
-            bad |= DF11_DEV_ERR_PAGES;
-            continue;
+                for (int x = 1; x < 32; x <<= 1) {
+                    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, x);
+                    if (lane >= x) incl += o;
+                }
+                __syncthreads();
+                if (lane == 31) S.sums[warp] = incl;
+                __syncthreads();
+                int before = base;
+                for (int i = 0; i < kPrefillThreads / 32; ++i) {
+                    if (i < warp) before += S.sums[i];
+                    base += S.sums[i];
+                }
+                const int at = before + incl - w;
+                if (pass && w && at <= want && want < at + w) {
+                    S.req = b + tid;
+                    S.pair = want - at;
+                }
+            }
+            if (!pass) {
+                all = base;
+                want = all - 1 - static_cast<int>(blockIdx.x);
+                if (want < 0) return;
+            }
         }
-        const uint8_t *blk = P.pages + (static_cast<uint64_t>(id) * P.kv_heads + h) * P.block.bytes;
-        const uint32_t off = static_cast<uint32_t>(j) & ((1u << P.page_shift) - 1u), b = lane * E / 16;
-        // the lane's E codes in the low bits of the aligned word that holds them
-        const uint32_t byte = lane * (E / 2), sh = 8 * (byte & 3u);
-        const uint32_t kw =
-            *reinterpret_cast<const uint32_t *>(blk + P.block.k_codes + off * (D / 2) + (byte & ~3u)) >> sh;
-        const uint32_t vw = *reinterpret_cast<const uint32_t *>(blk + P.block.v_codes +
-                                                                (((off >> 2) * (D / 16) + b) * 4u + (off & 3u)) * 8u +
-                                                                (byte & 4u)) >> sh;
-        const uint32_t ks = e4m3x2_to_f16x2(blk[P.block.k_scales + off * (D / 16) + b] * 0x0101u);
-        const uint32_t vs = e4m3x2_to_f16x2(blk[P.block.v_scales + (b << P.page_shift) + off] * 0x0101u);
-        uint32_t kr[4], vr[4];
-        e2m1x8_to_f16(kw, kr);
-        e2m1x8_to_f16(vw, vr);
-        float s = 0.0f, v[E];
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            float a, c;
-            f16x2_to_f32(f16x2_mul(kr[i], ks), a, c);
-            s += q[2 * i] * a + q[2 * i + 1] * c;
-            f16x2_to_f32(f16x2_mul(vr[i], vs), v[2 * i], v[2 * i + 1]);
-        }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-        const float mn = fmaxf(m, s), c = __expf(m - mn), p = __expf(s - mn);
-        m = mn;
-        l = l * c + p;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = o[i] * c + p * v[i];
     }
-    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = o[i];
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.q_full[i], 128);
+            mbar_init(&S.k_full[i], 128);
+            mbar_init(&S.k_empty[i], 1);
+            mbar_init(&S.v_full[i], 128);
+            mbar_init(&S.v_empty[i], 1);
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_full[i], 128);
+            mbar_init(&S.o_done[i], 1);
+        }
+        mbar_init(&S.end, 1);
+        S.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        tmem_alloc(&S.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
-    if (bad && P.err) atomicOr(P.err, static_cast<int>(bad));
-    float mm = -INFINITY, ll = 0.0f;
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_m[w]);
-    for (int w = 0; w < 4; ++w) ll += s_l[w] > 0.0f ? s_l[w] * __expf(s_m[w] - mm) : 0.0f;
-    for (int d = threadIdx.x; d < D; d += 128) {
-        float y = 0.0f;
-        for (int w = 0; w < 4; ++w) y += s_l[w] > 0.0f ? s_o[w][d] * __expf(s_m[w] - mm) : 0.0f;
-        static_cast<__nv_bfloat16 *>(A.o)[t * static_cast<int64_t>(A.o_token_stride) + hq * D + d] =
-            __float2bfloat16_rn(ll > 0.0f ? y / ll * P.v_scale : 0.0f);
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const PrefillWork W = prefill_work(P, S.req, S.pair);
+    uint32_t err = 0;
+
+    if (warp < 8) {
+        // =============================== softmax of tile x, a thread per row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        const int x = warp >> 2, r = tid & 127;
+        const int row = W.row0 + x * kPrefillTile + r;
+        const bool live = row < W.rows;
+        const int64_t token = W.q0 + row / group;
+        const int hq = head * group + row % group;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's TMEM lanes
+        const uint32_t s_col = tmem + lanes + x * kPrefillTile, o_col = tmem + lanes + 2 * kPrefillTile + x * D;
+        const int steps = W.a1[x] - W.a0[x];
+        float f = 0.0f;
+        if (steps) {
+            // the row's queries, scaled by a power of two into FP16's range
+            // (and by the sign of the scores' factor, which is then >= 0)
+            const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(A.q) +
+                                                              token * static_cast<int64_t>(A.q_token_stride) + hq * D);
+            float top = 0.0f;
+            if (live) {
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = __ldg(qp + i);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+                }
+            }
+            const uint32_t field = __float_as_uint(top) >> 23;
+            const int e = top == 0.0f || field == 255u ? 0 : max(static_cast<int>(field) - 127, -126);
+            const float f0 = A.scale * P.k_scale * 1.44269504088896341f;
+            float down = e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            if (f0 < 0.0f) down = -down;
+            f = fabsf(f0) * __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+            if (f == 0.0f) f = 1.0f, down = 0.0f;  // all scores 0, and still -inf where masked
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (live) v = __ldg(qp + i);
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
+                *reinterpret_cast<uint4 *>(S.q[x] + (i / 8) * (kPrefillTile * 128) + swz_chunk(r, i % 8)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&S.q_full[x]);
+        }
+        int64_t lo = 0, hi = 0;
+        if (live) prefill_row(P, W, row, lo, hi);
+        float m = -INFINITY, l = 0.0f;
+        bool run = true;
+        for (int it = 0; it < steps; ++it) {
+            const int j = W.a0[x] + it;
+            const int64_t key0 = static_cast<int64_t>(W.first + j) * kPrefillTile;
+            run = __all_sync(0xFFFFFFFFu, prefill_wait(&S.s_full[x], it & 1u, S, P.wait_ns));
+            if (!run) break;
+            tc_fence_after();
+            uint32_t s[kPrefillTile];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc_ld32(s_col + 32 * i, s + 32 * i);
+            // keys [a, b) of the step seen by this row
+            const int a = static_cast<int>(min(max(lo - key0, static_cast<int64_t>(0)), static_cast<int64_t>(kPrefillTile)));
+            const int b = static_cast<int>(min(max(hi - key0, static_cast<int64_t>(0)), static_cast<int64_t>(kPrefillTile)));
+            uint32_t seen[4];
+            bool full = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ai = min(max(a - 32 * i, 0), 32), bi = min(max(b - 32 * i, 0), 32);
+                const uint32_t below = bi == 32 ? 0xFFFFFFFFu : (1u << bi) - 1u;
+                seen[i] = (ai == 32 ? 0u : below & (0xFFFFFFFFu << ai)) &
+                          *reinterpret_cast<volatile uint32_t *>(&S.ok[j & 3][i]);
+                full &= seen[i] == 0xFFFFFFFFu;
+            }
+            tc_wait_ld();
+            if (__any_sync(0xFFFFFFFFu, !full)) {
+#pragma unroll
+                for (int i = 0; i < kPrefillTile; ++i)
+                    if (!(seen[i / 32] >> (i % 32) & 1u)) s[i] = 0xFF800000u;  // -inf
+            }
+            float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[1]), t2 = __uint_as_float(s[2]),
+                  t3 = __uint_as_float(s[3]);
+#pragma unroll
+            for (int i = 4; i < kPrefillTile; i += 4) {
+                t0 = fmaxf(t0, __uint_as_float(s[i]));
+                t1 = fmaxf(t1, __uint_as_float(s[i + 1]));
+                t2 = fmaxf(t2, __uint_as_float(s[i + 2]));
+                t3 = fmaxf(t3, __uint_as_float(s[i + 3]));
+            }
+            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+            const float mt = top == -INFINITY ? -INFINITY : top * f;
+            const bool grow = mt > m + kLazy || (m == -INFINITY && mt != -INFINITY);
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                const float mn = grow ? mt : m;
+                const float alpha = grow ? ex2(m - mn) : 1.0f;
+                m = mn;
+                l *= alpha;
+                if (it) {
+                    run = __all_sync(0xFFFFFFFFu, prefill_wait(&S.o_done[x], (it - 1) & 1u, S, P.wait_ns));
+                    if (!run) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < D; i += 16) {
+                        uint32_t o[16];
+                        tc_ld16(o_col + i, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+                        tc_st16(o_col + i, o);
+                    }
+                }
+            }
+            const float shift = m == -INFINITY ? 0.0f : m;
+            float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kPrefillTile; c += 32) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float p0 = ex2(fmaf(__uint_as_float(s[c + i]), f, -shift));
+                    const float p1 = ex2(fmaf(__uint_as_float(s[c + i + 1]), f, -shift));
+                    const float p2 = ex2(fmaf(__uint_as_float(s[c + i + 2]), f, -shift));
+                    const float p3 = ex2(fmaf(__uint_as_float(s[c + i + 3]), f, -shift));
+                    l0 += p0, l1 += p1, l2 += p2, l3 += p3;
+                    w[i / 2] = pack_f16(p0, p1);
+                    w[i / 2 + 1] = pack_f16(p2, p3);
+                }
+                tc_st16(s_col + c / 2, w);
+            }
+            l += (l0 + l1) + (l2 + l3);
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(&S.p_full[x]);
+        }
+        if (run && steps) {
+            run = __all_sync(0xFFFFFFFFu, prefill_wait(&S.o_done[x], (steps - 1) & 1u, S, P.wait_ns));
+            tc_fence_after();
+        }
+        if (!run) err |= DF11_DEV_ERR_TIMEOUT;
+        const float inv = run && l > 0.0f ? P.v_scale / l : 0.0f;
+        uint16_t *op = static_cast<uint16_t *>(A.o) + token * static_cast<int64_t>(A.o_token_stride) + hq * D;
+#pragma unroll
+        for (int i = 0; i < D; i += 16) {
+            uint32_t o[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = 0u;
+            if (steps) {
+                tc_ld16(o_col + i, o);
+                tc_wait_ld();
+            }
+            if (live) {
+#pragma unroll
+                for (int y = 0; y < 16; y += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        // l == 0: the row saw no key (its accumulator may hold anything finite or not)
+                        const float u = __uint_as_float(o[y + 2 * z]) * inv, v = __uint_as_float(o[y + 2 * z + 1]) * inv;
+                        w[z] = l > 0.0f || l != l ? bf16x2_of(u, v) : 0u;
+                    }
+                    *reinterpret_cast<uint4 *>(op + i + y) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        if (live && A.lse) A.lse[token * A.n_q_heads + hq] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        tc_fence_before();
+    } else if (warp < 12) {
+        // =============================== the cache to FP16 operand tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        constexpr uint32_t NB = D / 16;
+        const int u = tid - 256;  // K: the step's key; V: 8 keys and 16 elements
+        const int unit = u >> 3;  // V: 16 chunks of 8 keys x NB blocks, lanes of 8 over the chunks of one 128-byte row
+        const uint32_t vb = static_cast<uint32_t>(unit) % NB, vc = (static_cast<uint32_t>(unit) / NB) * 8u + (u & 7u);
+        const bool v_mine = vc < 16u;
+        const uint32_t mask = (1u << P.page_shift) - 1u;
+        auto block = [&](int64_t id, bool &have) -> const uint8_t * {
+            have = id >= 0 && static_cast<uint64_t>(id) < P.n_pages;
+            return P.pages + (static_cast<uint64_t>(have ? id : 0) * P.kv_heads + static_cast<uint32_t>(head)) * P.block.bytes;
+        };
+        uint32_t kw[D / 8], vw[16];
+        uint2 ks = make_uint2(0u, 0u), vs = make_uint2(0u, 0u);
+        bool k_have = false;
+        auto load_k = [&](int j, int64_t id) {
+            const int64_t key = static_cast<int64_t>(W.first + j) * kPrefillTile + u;
+            const uint8_t *b = block(id, k_have);
+            if (!k_have && id != kNoPage) err |= DF11_DEV_ERR_PAGES;
+#pragma unroll
+            for (uint32_t i = 0; i < D / 8; ++i) kw[i] = 0u;
+            ks = make_uint2(0u, 0u);
+            if (!k_have) return;
+            const uint32_t off = static_cast<uint32_t>(key) & mask;
+            const uint4 *c = reinterpret_cast<const uint4 *>(b + P.block.k_codes + off * (D / 2));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 v = __ldg(c + i);
+                kw[4 * i] = v.x, kw[4 * i + 1] = v.y, kw[4 * i + 2] = v.z, kw[4 * i + 3] = v.w;
+            }
+            if constexpr (D == 128) ks = __ldg(reinterpret_cast<const uint2 *>(b + P.block.k_scales + off * NB));
+            else ks.x = __ldg(reinterpret_cast<const uint32_t *>(b + P.block.k_scales + off * NB));
+        };
+        auto load_v = [&](int j, int64_t id) {
+            const int64_t key = static_cast<int64_t>(W.first + j) * kPrefillTile + 8 * vc;
+            bool have;
+            const uint8_t *b = block(id, have);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) vw[i] = 0u;
+            vs = make_uint2(0u, 0u);
+            if (!v_mine || !have) return;
+            const uint32_t off = static_cast<uint32_t>(key) & mask;
+            const uint8_t *c = b + P.block.v_codes + ((off >> 2) * NB + vb) * 32u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(c + (i / 2) * (NB * 32u)) + i % 2);
+                vw[4 * i] = v.x, vw[4 * i + 1] = v.y, vw[4 * i + 2] = v.z, vw[4 * i + 3] = v.w;
+            }
+            vs = __ldg(reinterpret_cast<const uint2 *>(b + P.block.v_scales + (vb << P.page_shift) + off));
+            // keys past the end may hold anything, NaN scales too: they count as 0
+            const int left = static_cast<int>(min(W.end - key, static_cast<int64_t>(8)));
+            if (left < 4) vs.x &= (1u << (8 * left)) - 1u;
+            if (left <= 4) vs.y = 0u;
+            else if (left < 8) vs.y &= (1u << (8 * (left - 4))) - 1u;
+        };
+        auto k_page = [&](int j) { return prefill_page(P, W, static_cast<int64_t>(W.first + j) * kPrefillTile + u); };
+        auto v_page = [&](int j) { return prefill_page(P, W, static_cast<int64_t>(W.first + j) * kPrefillTile + 8 * vc); };
+        int64_t idk = kNoPage, idv = kNoPage;
+        if (W.steps) {
+            load_k(0, k_page(0));
+            load_v(0, v_page(0));
+            if (W.steps > 1) idk = k_page(1), idv = v_page(1);
+        }
+        for (int j = 0; j < W.steps; ++j) {
+            const int st = j & 1;
+            if (j >= 2 && !__all_sync(0xFFFFFFFFu, prefill_wait(&S.k_empty[st], ((j >> 1) - 1) & 1u, S, P.wait_ns))) {
+                err |= DF11_DEV_ERR_TIMEOUT;
+                break;
+            }
+            {
+                const uint32_t ok = __ballot_sync(0xFFFFFFFFu, k_have);
+                if (lane == 0) S.ok[j & 3][warp - 8] = ok;
+                uint8_t *dst = S.k[st];
+#pragma unroll
+                for (uint32_t b = 0; b < NB; ++b) {
+                    const uint32_t sw = b < 4 ? ks.x : ks.y;
+                    const uint32_t two = e4m3x2_to_f16x2(__byte_perm(sw, 0, (b & 3u) * 0x11u));
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        uint32_t w[4];
+                        e2m1x8_to_f16(kw[2 * b + h], w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = f16x2_mul(w[i], two);
+                        const uint32_t c = 2 * b + h;
+                        *reinterpret_cast<uint4 *>(dst + (c / 8) * (kPrefillTile * 128) + swz_chunk(u, c % 8)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&S.k_full[st]);
+            if (j + 1 < W.steps) {
+                load_k(j + 1, idk);
+                if (j + 2 < W.steps) idk = k_page(j + 2);
+            }
+            if (j >= 2 && !__all_sync(0xFFFFFFFFu, prefill_wait(&S.v_empty[st], ((j >> 1) - 1) & 1u, S, P.wait_ns))) {
+                err |= DF11_DEV_ERR_TIMEOUT;
+                break;
+            }
+            if (v_mine) {
+                uint8_t *dst = S.v[st] + (vc / 8) * (D * 128);
+                const uint32_t sc[4] = {e4m3x2_to_f16x2(vs.x & 0xFFFFu), e4m3x2_to_f16x2(vs.x >> 16),
+                                        e4m3x2_to_f16x2(vs.y & 0xFFFFu), e4m3x2_to_f16x2(vs.y >> 16)};
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {
+                    uint32_t ev[4][4], od[4][4];  // [pair of keys][element / 2]
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a = vw[4 * i + h], b = vw[4 * i + 2 + h];
+                        e2m1x8_to_f16((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), ev[i]);
+                        e2m1x8_to_f16(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), od[i]);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            ev[i][z] = f16x2_mul(ev[i][z], sc[i]);
+                            od[i][z] = f16x2_mul(od[i][z], sc[i]);
+                        }
+                    }
+#pragma unroll
+                    for (uint32_t z = 0; z < 4; ++z) {
+                        const uint32_t d = 16 * vb + 8 * h + 2 * z;
+                        *reinterpret_cast<uint4 *>(dst + swz_chunk(d, vc % 8)) =
+                            make_uint4(ev[0][z], ev[1][z], ev[2][z], ev[3][z]);
+                        *reinterpret_cast<uint4 *>(dst + swz_chunk(d + 1, vc % 8)) =
+                            make_uint4(od[0][z], od[1][z], od[2][z], od[3][z]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&S.v_full[st]);
+            if (j + 1 < W.steps) {
+                load_v(j + 1, idv);
+                if (j + 2 < W.steps) idv = v_page(j + 2);
+            }
+        }
+    } else {
+        // =============================== MMAs
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        if (warp == 12 && lane == 0 && W.steps) {
+            // FP32 accumulate, FP16 A and B, M = 128; N = keys of a step, then head elements
+            constexpr uint32_t idesc_s = (1u << 4) | ((kPrefillTile >> 3) << 17) | ((128u >> 4) << 24);
+            constexpr uint32_t idesc_o = (1u << 4) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
+            bool run = true;
+            auto scores = [&](int x, int j) {
+                if (j == W.a0[x]) run = run && prefill_wait(&S.q_full[x], 0, S, P.wait_ns);
+                if (!run) return;
+                tc_fence_after();
+                const uint32_t q = smem_addr(S.q[x]), k = smem_addr(S.k[j & 1]);
+#pragma unroll
+                for (uint32_t i = 0; i < D / 16; ++i) {
+                    const uint32_t at = (i / 4) * (kPrefillTile * 128) + (i % 4) * 32;
+                    tc_mma(tmem + x * kPrefillTile, swz128_desc(q + at), swz128_desc(k + at), idesc_s, i > 0);
+                }
+                tc_commit(&S.s_full[x]);
+            };
+            auto values = [&](int x, int j) {
+                run = run && prefill_wait(&S.v_full[j & 1], (j >> 1) & 1u, S, P.wait_ns) &&
+                      prefill_wait(&S.p_full[x], (j - W.a0[x]) & 1u, S, P.wait_ns);
+                if (!run) return;
+                tc_fence_after();
+                const uint32_t v = smem_addr(S.v[j & 1]);
+#pragma unroll
+                for (uint32_t i = 0; i < kPrefillTile / 16; ++i)
+                    tc_mma_ts(tmem + 2 * kPrefillTile + x * D, tmem + x * kPrefillTile + i * 8,
+                              swz128_desc(v + (i / 4) * (D * 128) + (i % 4) * 32), idesc_o, i > 0 || j > W.a0[x]);
+                tc_commit(&S.o_done[x]);
+            };
+            auto active = [&](int x, int j) { return j >= W.a0[x] && j < W.a1[x]; };
+            for (int j = 0; j < W.steps && run; ++j) {
+                run = prefill_wait(&S.k_full[j & 1], (j >> 1) & 1u, S, P.wait_ns);
+                if (run && active(0, j)) scores(0, j);
+                if (run && j && active(1, j - 1)) values(1, j - 1);
+                if (run && j) tc_commit(&S.v_empty[(j - 1) & 1]);
+                if (run && active(1, j)) scores(1, j);
+                if (run) tc_commit(&S.k_empty[j & 1]);
+                if (run && active(0, j)) values(0, j);
+            }
+            if (run && active(1, W.steps - 1)) values(1, W.steps - 1);
+            // every MMA has completed before the CTA ends
+            tc_commit(&S.end);
+            if (!mbar_wait(&S.end, 0, P.wait_ns) || !run) err |= DF11_DEV_ERR_TIMEOUT;
+        }
+        __syncwarp();
     }
-    if (A.lse && threadIdx.x == 0)
-        A.lse[static_cast<int64_t>(t) * A.n_q_heads + hq] = ll > 0.0f ? mm + logf(ll) : -INFINITY;
+    err = __reduce_or_sync(0xFFFFFFFFu, err);
+    if (lane == 0) report(P.err, err);
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
 }
 
 // A multiprocessor each for the persistent CTAs; the workspace has room for kMaxCtas.
@@ -813,6 +1285,9 @@ AttnParams attn_params(const df11_kv4_cache &c, const df11_kv4_attention_args &a
     return P;
 }
 
+template <int D>
+constexpr size_t kPrefillSmem = sizeof(PrefillShared<D>) + 1024;  // and what aligns it
+
 bool prepare(int *sms) {
     constexpr int kDevices = 64;
     static std::mutex mu;
@@ -823,10 +1298,14 @@ bool prepare(int *sms) {
     if (!known[dev]) {
         int v = 0;
         if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
-        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(&attention_split_kernel<64>),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SplitShared<64>)) != cudaSuccess ||
-            cudaFuncSetAttribute(reinterpret_cast<const void *>(&attention_split_kernel<128>),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SplitShared<128>)) != cudaSuccess)
+        auto allow = [](auto *kernel, size_t bytes) {
+            return cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+        };
+        if (!allow(&attention_split_kernel<64>, sizeof(SplitShared<64>)) ||
+            !allow(&attention_split_kernel<128>, sizeof(SplitShared<128>)) ||
+            !allow(&attention_prefill_kernel<64>, kPrefillSmem<64>) ||
+            !allow(&attention_prefill_kernel<128>, kPrefillSmem<128>))
             return false;
         known[dev] = v;
     }
@@ -850,9 +1329,15 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
     if (c.head_dim == 128) attention_split_kernel<128><<<sms, kSplitThreads, sizeof(SplitShared<128>), s>>>(P);
     else attention_split_kernel<64><<<sms, kSplitThreads, sizeof(SplitShared<64>), s>>>(P);
     if (static_cast<int64_t>(a.max_q_len) * P.group > kSplitMaxRows) {
-        const dim3 grid(a.n_tokens, a.n_q_heads);
-        if (c.head_dim == 128) attention_rows_kernel<128><<<grid, 128, 0, s>>>(P);
-        else attention_rows_kernel<64><<<grid, 128, 0, s>>>(P);
+        // as many pairs of tiles as the rows can make: full ones, and a last
+        // one of each request that has more rows than the other path takes
+        const int64_t rows = static_cast<int64_t>(a.n_tokens) * P.group;
+        const int64_t pairs = rows / (2 * kPrefillTile) + std::min<int64_t>(a.n_reqs, rows / (kSplitMaxRows + 1));
+        if (pairs > INT32_MAX) return LaunchStatus::kInvalid;
+        const dim3 grid(static_cast<unsigned>(pairs), P.kv_heads);
+        if (pairs == 0) return LaunchStatus::kOk;
+        if (c.head_dim == 128) attention_prefill_kernel<128><<<grid, kPrefillThreads, kPrefillSmem<128>, s>>>(P);
+        else attention_prefill_kernel<64><<<grid, kPrefillThreads, kPrefillSmem<64>, s>>>(P);
     }
     return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;
 }
