@@ -40,23 +40,25 @@ struct AttnParams {
 // keys within a tile is free as long as both operands agree.  tcgen05 would
 // want the decoded tile written to shared memory with 128 rows of which 8
 // columns are used; here nothing decoded is ever stored.
-constexpr int kSplitWarps = 10;
+constexpr int kSplitWarps = 12;
 constexpr int kSplitThreads = 32 * kSplitWarps;
-constexpr int kSplitCols = 8;    // rows of a unit
-constexpr int kSplitKeys = 64;   // keys of a chunk: a warp's step, one stage of its ring
-constexpr int kSplitStages = 2;
+constexpr int kSplitCols = 8;      // rows of a unit
+constexpr int kSplitKeys = 64;     // keys of a chunk: a warp's step
 constexpr int kSplitMaxRows = 64;  // rows (tokens x heads of a group) of a request that go this way
+constexpr int kSplitAlign = 4 * kSplitWarps;  // units of at most so many chunks are not shared between CTAs
+constexpr int32_t kMaxKeys = INT32_MAX - 255;
 
 template <int D>
 struct SplitShared {
-    static constexpr uint32_t kStage = kSplitKeys * D * 9 / 8;
+    static constexpr uint32_t kHalf = kSplitKeys * D * 9 / 16;  // K or V of a chunk
     static constexpr int kPitch = D + 4;  // floats; spreads a thread's columns over the banks
-    alignas(128) uint8_t ring[kSplitWarps][kSplitStages][kStage];
+    alignas(128) uint8_t k[kSplitWarps][kHalf], v[kSplitWarps][kHalf];
     alignas(16) float o[kSplitWarps][kSplitCols][kPitch];
     float m[kSplitWarps][kSplitCols], l[kSplitWarps][kSplitCols];
-    alignas(8) uint64_t full[kSplitWarps][kSplitStages];
+    alignas(8) uint64_t k_full[kSplitWarps], v_full[kSplitWarps];
     int64_t sums[kSplitWarps];
-    int64_t total, start_off;
+    int64_t start_off, end;
+    int32_t longest[kSplitWarps];
     int32_t start_req, last;
 };
 
@@ -71,11 +73,16 @@ __host__ __device__ constexpr uint32_t split_partial_floats() {
 // request that sees no key still has one chunk, which writes its zeros.
 struct SplitReq {
     int32_t q0, n, rows, tiles, units, c_lo, chunks;
-    int64_t kv, begin;  // keys; the first that any row sees
+    int32_t kv, begin, end;  // keys; the first that any row sees; the last + 1 that the table holds
 };
 
 __device__ __forceinline__ bool rows_valid(const df11_kv4_attention_args &A, int q0, int q1) {
     return q0 >= 0 && q1 >= q0 && q1 <= A.n_tokens && q1 - q0 <= A.max_q_len;
+}
+
+// Keys that a request's block-table row has room for.
+__device__ __forceinline__ int32_t key_room(const AttnParams &P) {
+    return static_cast<int32_t>(min(static_cast<int64_t>(P.a.max_pages) << P.page_shift, static_cast<int64_t>(kMaxKeys)));
 }
 
 __device__ __forceinline__ SplitReq split_req(const AttnParams &P, int r) {
@@ -89,12 +96,11 @@ __device__ __forceinline__ SplitReq split_req(const AttnParams &P, int r) {
     if (rows == 0 || rows > kSplitMaxRows) return q;
     q.rows = static_cast<int32_t>(rows);
     q.tiles = (q.rows + kSplitCols - 1) / kSplitCols;
-    q.kv = max(__ldg(A.kv_lens + r), 0);
-    const int64_t cap = static_cast<int64_t>(A.max_pages) << P.page_shift;
-    const int64_t end = min(q.kv, cap);
-    q.begin = A.window ? min(max(q.kv - q.n + 1 - A.window, static_cast<int64_t>(0)), end) : 0;
-    q.c_lo = static_cast<int32_t>(q.begin / kSplitKeys);
-    q.chunks = max(static_cast<int32_t>((end + kSplitKeys - 1) / kSplitKeys) - q.c_lo, 1);
+    q.kv = min(max(__ldg(A.kv_lens + r), 0), kMaxKeys);
+    q.end = min(q.kv, key_room(P));
+    q.begin = A.window ? min(max(q.kv - q.n + 1 - A.window, 0), q.end) : 0;
+    q.c_lo = q.begin / kSplitKeys;
+    q.chunks = max((q.end + kSplitKeys - 1) / kSplitKeys - q.c_lo, 1);
     q.units = static_cast<int32_t>(P.kv_heads) * q.tiles;
     return q;
 }
@@ -123,6 +129,7 @@ struct SplitPos {
             load(P);
         }
     }
+    __device__ __forceinline__ int key0() const { return (q.c_lo + c) * kSplitKeys; }
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -158,7 +165,7 @@ template <int D>
 struct SplitUnit {
     uint32_t qb[D / 16][2];
     float f[2], m[2], l[2];
-    int64_t lo[2], hi[2], all_lo, all_hi, any_lo, any_hi;
+    int lo[2], hi[2], all_lo, all_hi, any_lo, any_hi;
     float o[D / 16][4];
 };
 
@@ -169,14 +176,14 @@ struct SplitUnit {
 template <int D>
 __device__ __forceinline__ void split_load_unit(const AttnParams &P, const SplitPos &at, int lane, SplitUnit<D> &U) {
     const df11_kv4_attention_args &A = P.a;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3, group = static_cast<int>(P.group);
     const int tile = at.tile, row = tile * kSplitCols + g;
     float x[D / 4];
     if (row < at.q.rows) {
         const uint4 *p = reinterpret_cast<const uint4 *>(
             static_cast<const uint16_t *>(A.q) +
-            static_cast<int64_t>(at.q.q0 + row / static_cast<int>(P.group)) * static_cast<int64_t>(A.q_token_stride) +
-            (at.head * static_cast<int>(P.group) + row % static_cast<int>(P.group)) * D + t * (D / 4));
+            static_cast<int64_t>(at.q.q0 + row / group) * static_cast<int64_t>(A.q_token_stride) +
+            (at.head * group + row % group) * D + t * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
             const uint4 v = __ldg(p + i);
@@ -205,10 +212,7 @@ __device__ __forceinline__ void split_load_unit(const AttnParams &P, const Split
         U.qb[j][0] = pack_f16(x[4 * j] * down, x[4 * j + 1] * down);
         U.qb[j][1] = pack_f16(x[4 * j + 2] * down, x[4 * j + 3] * down);
     }
-    U.all_lo = 0;
-    U.all_hi = INT64_MAX;
-    U.any_lo = INT64_MAX;
-    U.any_hi = 0;
+    const int base = at.q.kv - at.q.n;  // the key position of the request's row 0
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int col = 2 * t + i, ec = __shfl_sync(0xFFFFFFFFu, e, 4 * col);
@@ -217,24 +221,20 @@ __device__ __forceinline__ void split_load_unit(const AttnParams &P, const Split
         U.l[i] = 0.0f;
         const int rc = tile * kSplitCols + col;
         U.lo[i] = 0;
-        U.hi[i] = INT64_MAX;
+        U.hi[i] = INT32_MAX;
         if (rc < at.q.rows) {
-            const int64_t pos = at.q.kv - at.q.n + rc / static_cast<int>(P.group);
-            U.hi[i] = max(A.causal ? pos + 1 : at.q.kv, static_cast<int64_t>(0));
-            U.lo[i] = A.window ? max(pos + 1 - A.window, static_cast<int64_t>(0)) : 0;
+            const int pos = base + rc / group;
+            if (A.causal) U.hi[i] = pos + 1;
+            if (A.window) U.lo[i] = pos + 1 - A.window;
         }
     }
-    {
-        // what every row of the tile sees, and what any does (rows ascend)
-        const int r0 = tile * kSplitCols, r1 = min(r0 + kSplitCols, at.q.rows) - 1;
-        const int64_t p0 = at.q.kv - at.q.n + r0 / static_cast<int>(P.group);
-        const int64_t p1 = at.q.kv - at.q.n + r1 / static_cast<int>(P.group);
-        const int64_t cap = static_cast<int64_t>(A.max_pages) << P.page_shift, end = min(at.q.kv, cap);
-        U.all_hi = min(A.causal ? p0 + 1 : end, end);
-        U.any_hi = min(A.causal ? p1 + 1 : end, end);
-        U.all_lo = A.window ? p1 + 1 - A.window : 0;
-        U.any_lo = A.window ? max(p0 + 1 - A.window, static_cast<int64_t>(0)) : 0;
-    }
+    // what every row of the tile sees, and what any does (rows ascend)
+    const int p0 = base + tile * kSplitCols / group;
+    const int p1 = base + (min((tile + 1) * kSplitCols, at.q.rows) - 1) / group;
+    U.all_hi = A.causal ? min(p0 + 1, at.q.end) : at.q.end;
+    U.any_hi = A.causal ? min(p1 + 1, at.q.end) : at.q.end;
+    U.all_lo = A.window ? p1 + 1 - A.window : 0;
+    U.any_lo = A.window ? max(p0 + 1 - A.window, 0) : 0;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -246,126 +246,118 @@ __device__ __forceinline__ void split_load_unit(const AttnParams &P, const Split
 // by halves: page 0 of the chunk is the half.
 constexpr int64_t kNoPage = INT64_MIN;
 
+template <int ES>
 __device__ __forceinline__ int64_t split_page(const AttnParams &P, const SplitPos &at, int lane) {
-    const int eps_shift = min(static_cast<int>(P.page_shift), 6);
-    const int64_t key = static_cast<int64_t>(at.q.c_lo + at.c) * kSplitKeys + (static_cast<int64_t>(lane) << eps_shift);
-    const int64_t pg = key >> P.page_shift;
-    if ((lane << eps_shift) >= kSplitKeys || key >= at.q.kv || key + (1 << eps_shift) <= at.q.begin ||
-        pg >= P.a.max_pages)
-        return kNoPage;
+    const int key = at.key0() + (lane << ES), pg = key >> P.page_shift;
+    if (lane >= (kSplitKeys >> ES) || key >= at.q.end || key + (1 << ES) <= at.q.begin) return kNoPage;
     return __ldg(P.a.block_table + static_cast<int64_t>(at.r) * P.a.max_pages + pg);
 }
 
-// Copies a chunk's pages (of the unit's head) into a stage, each as its own
-// block of min(page_size, 64) tokens.  Returns the mask of the pages that are
-// there (bit p, all lanes); flags bad entries.
-template <int D>
-__device__ __forceinline__ uint32_t split_issue(const AttnParams &P, const SplitPos &at, int64_t id, int lane,
-                                                uint8_t *stage, uint64_t *bar, uint32_t &err) {
-    const bool have = id >= 0 && static_cast<uint64_t>(id) < P.n_pages;
-    if (!have && id != kNoPage) err |= DF11_DEV_ERR_PAGES;
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, have);
-    const uint8_t *src =
-        P.pages + (static_cast<uint64_t>(have ? id : 0) * P.kv_heads + static_cast<uint32_t>(at.head)) * P.block.bytes;
-    if (P.page_shift <= 6) {
-        const uint32_t bytes = P.block.bytes;
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * bytes);
+// Copies the K (or V) halves of a chunk's pages, of the unit's head, into
+// shared memory, each as the half of a block of 2^ES tokens.
+template <int D, int ES>
+__device__ __forceinline__ void split_issue(const AttnParams &P, const uint8_t *block, bool v, bool have, uint32_t mask,
+                                            int half, int lane, uint8_t *dst, uint64_t *bar) {
+    constexpr Kv4Block B = kv4_block(1u << ES, D);
+    if (ES < 6 || P.page_shift == 6) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * B.v_codes);
         __syncwarp();
-        if (have) bulk_load(stage + lane * bytes, src, bytes, bar);
+        if (have) bulk_load(dst + lane * B.v_codes, block + (v ? B.v_codes : 0u), B.v_codes, bar);
     } else {
-        // half of a 128-token page: its rows of the three row-ordered sections
-        // are contiguous, the V scales are 64 bytes of each block's 128
-        constexpr Kv4Block H = kv4_block(64, D);
-        const uint32_t half = static_cast<uint32_t>((at.q.c_lo + at.c) & 1);
-        if (lane == 0) mbar_arrive_expect_tx(bar, mask ? H.bytes : 0);
-        const uint64_t base = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(src), 0);
-        const uint8_t *s0 = reinterpret_cast<const uint8_t *>(base);
-        __syncwarp();
-        if (mask) {
-            if (lane == 0) bulk_load(stage, s0 + half * H.k_scales, H.k_scales, bar);
-            if (lane == 1)
-                bulk_load(stage + H.k_scales, s0 + P.block.k_scales + half * (H.v_codes - H.k_scales),
-                          H.v_codes - H.k_scales, bar);
-            if (lane == 2)
-                bulk_load(stage + H.v_codes, s0 + P.block.v_codes + half * (H.v_scales - H.v_codes),
-                          H.v_scales - H.v_codes, bar);
-            if (lane >= 3 && lane < 3 + D / 16)
-                bulk_load(stage + H.v_scales + (lane - 3) * 64, s0 + P.block.v_scales + (lane - 3) * 128 + half * 64, 64,
-                          bar);
-        }
+        // half of a 128-token page: its rows of the row-ordered sections are
+        // contiguous, the V scales are 64 bytes of each element block's 128
+        if (lane == 0) mbar_arrive_expect_tx(bar, mask ? B.v_codes : 0u);
+        const uint8_t *s = reinterpret_cast<const uint8_t *>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(block), 0));
+        constexpr uint32_t codes = B.k_scales, scales = B.v_codes - B.k_scales;
+        if (mask && lane == 0) bulk_load(dst, s + (v ? P.block.v_codes : 0u) + half * codes, codes, bar);
+        if (mask && lane == 1 && !v) bulk_load(dst + codes, s + P.block.k_scales + half * scales, scales, bar);
+        if (mask && v && lane >= 1 && lane < 1 + D / 16)
+            bulk_load(dst + codes + (lane - 1) * 64, s + P.block.v_scales + (lane - 1) * 128 + half * 64, 64, bar);
     }
-    return mask;
 }
 
-// One chunk: scores of 64 keys, their softmax against the running maximum, and
-// the products with V.
-template <int D>
-__device__ __forceinline__ void split_chunk(const AttnParams &P, const uint8_t *stage, int64_t key0, uint32_t pages,
-                                            int lane, SplitUnit<D> &U) {
+// The scores of a chunk's 64 keys, in log2 units; what a row does not see is -inf.
+template <int D, int ES>
+__device__ __forceinline__ void split_scores(const uint8_t *stage, int key0, uint32_t pages, bool whole, int lane,
+                                             const SplitUnit<D> &U, float (&s)[4][4]) {
     constexpr int KW = D / 32;  // words of a thread's K codes of one key
+    constexpr Kv4Block B = kv4_block(1u << ES, D);
     const int g = lane >> 2, t = lane & 3;
-    const int eps_shift = min(static_cast<int>(P.page_shift), 6);
-    const uint32_t eps = 1u << eps_shift;
-    const Kv4Block B = kv4_block(eps, D);
-    const bool whole = pages == (1u << (kSplitKeys >> eps_shift)) - 1u && key0 >= U.all_lo &&
-                       key0 + kSplitKeys <= U.all_hi;
     // rows g and g + 8 of a tile of 16 keys are keys kg and kg + 2, so that
     // the 4 slots of the second product that a thread holds are 4 consecutive keys
     const uint32_t kg = 4u * (static_cast<uint32_t>(g) >> 1) + (g & 1u);
-    float s[4][4];
+    const uint8_t *codes = stage + kg * (D / 2) + t * (D / 8);
+    const uint8_t *scales = stage + B.k_scales + kg * (D / 16) + (D == 128 ? 2 * t : t);
+    // two tiles at a time, two accumulators each: four chains of MMAs that do
+    // not wait for one another
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t in = 16u * i;
-        const uint8_t *blk = stage + (in >> eps_shift) * B.bytes;
-        const uint32_t off = in & (eps - 1u);
-        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-        uint32_t w[2][KW], sc[2][KW / 2 ? KW / 2 : 1];
+    for (int i = 0; i < 4; i += 2) {
+        float acc[2][2][4];
+        uint32_t w[2][2][KW], sc[2][2][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t k = off + kg + 2u * r;
-            const uint8_t *c = blk + B.k_codes + k * (D / 2) + t * (D / 8);
-            if constexpr (D == 128) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(c);
-                w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-                const uint32_t two = e4m3x2_to_f16x2(
-                    *reinterpret_cast<const uint16_t *>(blk + B.k_scales + k * (D / 16) + 2 * t));
-                sc[r][0] = __byte_perm(two, 0, 0x1010);
-                sc[r][1] = __byte_perm(two, 0, 0x3232);
-            } else {
-                const uint2 v = *reinterpret_cast<const uint2 *>(c);
-                w[r][0] = v.x, w[r][1] = v.y;
-                sc[r][0] = e4m3x2_to_f16x2(blk[B.k_scales + k * (D / 16) + t] * 0x0101u);
+        for (int z = 0; z < 2; ++z) {
+            const uint32_t page = (16u * (i + z)) >> ES, off = (16u * (i + z)) & ((1u << ES) - 1u);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint8_t *c = codes + page * B.v_codes + (off + 2u * r) * (D / 2);
+                const uint8_t *x = scales + page * B.v_codes + (off + 2u * r) * (D / 16);
+                if constexpr (D == 128) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(c);
+                    w[z][r][0] = v.x, w[z][r][1] = v.y, w[z][r][2] = v.z, w[z][r][3] = v.w;
+                    const uint32_t two = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(x));
+                    sc[z][r][0] = __byte_perm(two, 0, 0x1010);
+                    sc[z][r][1] = __byte_perm(two, 0, 0x3232);
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(c);
+                    w[z][r][0] = v.x, w[z][r][1] = v.y;
+                    sc[z][r][0] = e4m3x2_to_f16x2(*x * 0x0101u);
+                }
             }
+#pragma unroll
+            for (int y = 0; y < 8; ++y) acc[z][y / 4][y % 4] = 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < KW; ++j) {
-            uint32_t a[2][4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                e2m1x8_to_f16(w[r][j], a[r]);
+            for (int z = 0; z < 2; ++z) {
+                uint32_t a[2][4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) a[r][x] = f16x2_mul(a[r][x], sc[r][j / 2]);
+                for (int r = 0; r < 2; ++r) {
+                    e2m1x8_to_f16(w[z][r][j], a[r]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) a[r][x] = f16x2_mul(a[r][x], sc[z][r][j / 2]);
+                }
+                mma16816(acc[z][0], a[0][0], a[1][0], a[0][1], a[1][1], U.qb[2 * j][0], U.qb[2 * j][1]);
+                mma16816(acc[z][1], a[0][2], a[1][2], a[0][3], a[1][3], U.qb[2 * j + 1][0], U.qb[2 * j + 1][1]);
             }
-            mma16816(s[i], a[0][0], a[1][0], a[0][1], a[1][1], U.qb[2 * j][0], U.qb[2 * j][1]);
-            mma16816(s[i], a[0][2], a[1][2], a[0][3], a[1][3], U.qb[2 * j + 1][0], U.qb[2 * j + 1][1]);
         }
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[i + z][x] = (acc[z][0][x] + acc[z][1][x]) * U.f[x & 1];
     }
-    // scores in log2 units; what a row does not see is -inf
-    float top[2] = {-INFINITY, -INFINITY};
+    if (!whole) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            s[i][x] *= U.f[x & 1];
-            if (!whole) {
+            for (int x = 0; x < 4; ++x) {
                 const uint32_t in = 16u * i + kg + (x & 2u);
-                const int64_t key = key0 + in;
-                if (!(pages >> (in >> eps_shift) & 1u) || key < U.lo[x & 1] || key >= U.hi[x & 1] || key >= U.any_hi)
+                const int key = key0 + static_cast<int>(in);
+                if (!(pages >> (in >> ES) & 1u) || key < U.lo[x & 1] || key >= U.hi[x & 1] || key >= U.any_hi)
                     s[i][x] = -INFINITY;
             }
-            top[x & 1] = fmaxf(top[x & 1], s[i][x]);
-        }
     }
+}
+
+// Softmax of the scores against the running maximum; the probabilities as the
+// B operand of the second product.
+template <int D>
+__device__ __forceinline__ void split_softmax(float (&s)[4][4], SplitUnit<D> &U, uint32_t (&pb)[4][2]) {
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top[x & 1] = fmaxf(top[x & 1], s[i][x]);
     bool moved = false;
     float shift[2], alpha[2];
 #pragma unroll
@@ -385,7 +377,6 @@ __device__ __forceinline__ void split_chunk(const AttnParams &P, const uint8_t *
 #pragma unroll
             for (int x = 0; x < 4; ++x) U.o[i][x] *= alpha[x & 1];
     }
-    uint32_t pb[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -397,21 +388,29 @@ __device__ __forceinline__ void split_chunk(const AttnParams &P, const uint8_t *
         pb[i][0] = transpose8x8(pack_f16(s[i][0], s[i][1]));
         pb[i][1] = transpose8x8(pack_f16(s[i][2], s[i][3]));
     }
+}
+
+// O^T += V^T P^T over the chunk's keys.
+template <int D, int ES>
+__device__ __forceinline__ void split_values(const uint8_t *stage, int key0, uint32_t pages, bool whole, int lane,
+                                             SplitUnit<D> &U, const uint32_t (&pb)[4][2]) {
+    constexpr Kv4Block B = kv4_block(1u << ES, D);
+    const int g = lane >> 2, t = lane & 3;
+    const int b = D == 128 ? g : g >> 1;  // the scale block of the thread's elements [g D / 8, (g + 1) D / 8)
+    const uint8_t *codes = stage + (t * (D / 16) + b) * 32;
+    const uint8_t *scales = stage + B.k_scales + (b << ES) + 4 * t;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t in = 16u * i;
-        const uint8_t *blk = stage + (in >> eps_shift) * B.bytes;
-        const uint32_t off = in & (eps - 1u);
-        const int b = D == 128 ? g : g >> 1;  // the scale block of the thread's elements [g D / 8, (g + 1) D / 8)
-        const uint8_t *c = blk + B.v_codes + (((off >> 2) + t) * (D / 16) + b) * 32u;
-        uint32_t vs = *reinterpret_cast<const uint32_t *>(blk + B.v_scales + (b << eps_shift) + off + 4 * t);
+        const uint32_t in = 16u * i, page = in >> ES, off = in & ((1u << ES) - 1u);
+        const uint8_t *c = codes + page * B.v_codes + (off >> 2) * (D / 16) * 32u;
+        uint32_t vs = *reinterpret_cast<const uint32_t *>(scales + page * B.v_codes + off);
         if (!whole) {
             // a key that no row sees may hold anything, NaN scales too: 0 times NaN must not reach a sum
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const uint32_t k = in + 4 * t + x;
-                const int64_t key = key0 + k;
-                if (!(pages >> (k >> eps_shift) & 1u) || key < U.any_lo || key >= U.any_hi) vs &= ~(0xFFu << (8 * x));
+                const int key = key0 + static_cast<int>(k);
+                if (!(pages >> (k >> ES) & 1u) || key < U.any_lo || key >= U.any_hi) vs &= ~(0xFFu << (8 * x));
             }
         }
         const uint32_t sc[2] = {e4m3x2_to_f16x2(vs & 0xFFFFu), e4m3x2_to_f16x2(vs >> 16)};
@@ -470,38 +469,43 @@ __device__ __forceinline__ void split_store(const AttnParams &P, const SplitPos 
 // Persistent CTAs, each a contiguous, equal share of the launch's chunks
 // (request, unit, chunk in order), so a long request spreads over the GPU and
 // short ones share a CTA, whatever the mix.  A share's chunks go to the warps
-// in turn; each warp keeps a ring of stages that its own bulk copies fill, two
-// chunks ahead and across unit ends.  At the end of a unit (or of the share)
-// the warps' results are joined in shared memory; a unit that spans CTAs goes
-// through the workspace, and the CTA that arrives last joins its parts in
-// order: no CTA waits for another, and the result does not depend on which
-// one was last.
-template <int D>
+// in turn; each warp has room for one chunk in shared memory, and refills its
+// K half as soon as the scores are taken and its V half after the second
+// product, with the next chunk, across unit ends.  At the end of a unit (or of
+// the share) the warps' results are joined in shared memory; a unit that spans
+// CTAs goes through the workspace, and the CTA that arrives last joins its
+// parts in order: no CTA waits for another, and the result does not depend on
+// which one was last.  Where all units are short (kSplitAlign), a unit goes to
+// the CTA that has its first chunk: fewer CTAs, but no join between them.
+template <int D, int ES>
 __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     SplitShared<D> &S = *reinterpret_cast<SplitShared<D> *>(smem_raw);
     const df11_kv4_attention_args &A = P.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t err = 0;
-    if (lane == 0)
-        for (int i = 0; i < kSplitStages; ++i) mbar_init(&S.full[warp][i], 1);
-    fence_mbar_init();
+    if (lane == 0) {
+        mbar_init(&S.k_full[warp], 1);
+        mbar_init(&S.v_full[warp], 1);
+        fence_mbar_init();
+    }
 
     // ---- the launch's chunks, and the request in which this CTA's share starts
-    auto weight = [&](int r) -> int64_t {
-        if (r >= A.n_reqs) return 0;
-        const SplitReq q = split_req(P, r);
-        return static_cast<int64_t>(q.units) * q.chunks;
-    };
-    const bool one = A.n_reqs <= kSplitThreads;
     int64_t mine = 0;
-    for (int r = tid; r < A.n_reqs; r += kSplitThreads) mine += weight(r);
-    if (blockIdx.x == 0)
-        for (int r = tid; r < A.n_reqs; r += kSplitThreads) {
+    int longest = 0;
+    const int room = key_room(P);
+    for (int r = tid; r < A.n_reqs; r += kSplitThreads) {
+        const SplitReq q = split_req(P, r);
+        mine += static_cast<int64_t>(q.units) * q.chunks;
+        if (q.units) longest = max(longest, q.chunks);
+        if (blockIdx.x == 0) {
             if (!rows_valid(A, __ldg(A.q_start + r), __ldg(A.q_start + r + 1))) err |= DF11_DEV_ERR_AUX;
-            if (static_cast<int64_t>(__ldg(A.kv_lens + r)) > static_cast<int64_t>(A.max_pages) << P.page_shift)
-                err |= DF11_DEV_ERR_PAGES;
+            if (__ldg(A.kv_lens + r) > room) err |= DF11_DEV_ERR_PAGES;
         }
+    }
+    const int longest_mine = longest;  // with a thread per request, that request's chunks
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    if (lane == 0) S.longest[warp] = longest;
     auto block_scan = [&](int64_t v, int64_t &all) -> int64_t {  // exclusive
         int64_t incl = v;
 #pragma unroll
@@ -514,35 +518,50 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
         __syncthreads();
         int64_t before = 0;
         all = 0;
+#pragma unroll
         for (int w = 0; w < kSplitWarps; ++w) {
             if (w < warp) before += S.sums[w];
             all += S.sums[w];
         }
         return before + incl - v;
     };
-    int64_t total, at0 = block_scan(mine, total);
+    int64_t total;
+    const int64_t at0 = block_scan(mine, total);
+#pragma unroll
+    for (int w = 0; w < kSplitWarps; ++w) longest = max(longest, S.longest[w]);
+    const bool aligned = longest <= kSplitAlign;
     // no share is empty: a unit's parts are then those of every CTA from its first to its last
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
     if (blockIdx.x >= ctas) {
         report(P.err, err);
         return;
     }
-    const int64_t x0 = total * blockIdx.x / ctas, x1 = total * (blockIdx.x + 1) / ctas;
-    if (one) {
-        if (mine && at0 <= x0 && x0 < at0 + mine) {
-            S.start_req = tid;
-            S.start_off = x0 - at0;
+    int64_t x0 = total * blockIdx.x / ctas, x1 = total * (blockIdx.x + 1) / ctas;
+    // a request that holds the share's first or (aligned) last position, its chunks from `at` on, says where in it that is
+    auto place = [&](int r, int64_t at, int64_t weight, int chunks) {
+        if (!weight) return;
+        if (at <= x0 && x0 < at + weight) {
+            S.start_req = r;
+            S.start_off = x0 - at;
         }
+        if (aligned && at < x1 && x1 < at + weight) S.end = at + (x1 - at + chunks - 1) / chunks * chunks;
+    };
+    if (tid == 0) S.end = x1;
+    if (A.n_reqs <= kSplitThreads) {
+        __syncthreads();
+        place(tid, at0, mine, longest_mine);
     } else {
         int64_t base = 0;
-        for (int b = 0; b < A.n_reqs && base <= x0; b += kSplitThreads) {
-            const int64_t v = weight(b + tid);
-            int64_t all;
-            const int64_t at = base + block_scan(v, all);
-            if (v && at <= x0 && x0 < at + v) {
-                S.start_req = b + tid;
-                S.start_off = x0 - at;
+        for (int b = 0; b < A.n_reqs && base <= x1; b += kSplitThreads) {
+            int64_t v = 0, all;
+            int chunks = 1;
+            if (b + tid < A.n_reqs) {
+                const SplitReq q = split_req(P, b + tid);
+                v = static_cast<int64_t>(q.units) * q.chunks;
+                chunks = q.chunks;
             }
+            const int64_t at = base + block_scan(v, all);
+            place(b + tid, at, v, chunks);
             base += all;
         }
     }
@@ -550,65 +569,110 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     SplitPos seg;  // the unit being computed, at the share's first chunk of it
     seg.r = S.start_req;
     seg.q = split_req(P, seg.r);
-    const int unit = static_cast<int>(S.start_off / seg.q.chunks);
-    seg.head = unit / seg.q.tiles;
-    seg.tile = unit % seg.q.tiles;
-    seg.c = static_cast<int>(S.start_off % seg.q.chunks);
-    // the copies run ahead of the computation on their own position
-    SplitPos ahead = seg;
-    int64_t ax = x0 + warp, cx = x0 + warp;  // this warp's next chunk to copy, to compute
-    uint32_t have[kSplitStages];
-    uint32_t issued = 0, used = 0;
-    int64_t id = kNoPage;
-    if (ax < x1) {
-        ahead.advance(P, warp);
-        id = split_page(P, ahead, lane);
+    {
+        const int64_t off = S.start_off;
+        const int unit = static_cast<int>(off / seg.q.chunks);
+        seg.head = unit / seg.q.tiles;
+        seg.tile = unit % seg.q.tiles;
+        seg.c = static_cast<int>(off % seg.q.chunks);
     }
-    auto issue = [&]() {
-        const uint32_t st = issued % kSplitStages;
-        const uint32_t got = split_issue<D>(P, ahead, id, lane, S.ring[warp][st], &S.full[warp][st], err);
-#pragma unroll
-        for (int i = 0; i < kSplitStages; ++i)
-            if (st == static_cast<uint32_t>(i)) have[i] = got;
-        ++issued;
-        ax += kSplitWarps;
-        if (ax < x1) {
-            ahead.advance(P, kSplitWarps);
-            id = split_page(P, ahead, lane);
+    if (aligned) {
+        x1 = S.end;
+        if (seg.c) {
+            const int skip = seg.q.chunks - seg.c;
+            x0 += skip;
+            if (x0 < x1) seg.advance(P, skip);
+        }
+        if (x0 >= x1) {
+            report(P.err, err);
+            return;
+        }
+    }
+
+    // ---- this warp's copies, one chunk ahead of its computation
+    SplitPos ahead = seg;
+    int64_t ax = x0, cx = x0 + warp, x = x0;  // the launch's index of ahead, of this warp's next chunk, of seg
+    bool next = false;  // there is a chunk at `ahead` for this warp
+    uint32_t next_pages = 0, parity = 0;
+    const uint8_t *next_block = nullptr;
+    bool next_have = false;
+    int64_t id = kNoPage;
+    auto seek = [&](int by) {
+        ax += by;
+        next = ax < x1;
+        if (next) {
+            ahead.advance(P, by);
+            id = split_page<ES>(P, ahead, lane);
         }
     };
-    for (int i = 0; i < kSplitStages; ++i)
-        if (ax < x1) issue();
+    auto take_pages = [&]() {
+        next_have = id >= 0 && static_cast<uint64_t>(id) < P.n_pages;
+        if (!next_have && id != kNoPage) err |= DF11_DEV_ERR_PAGES;
+        next_pages = __ballot_sync(0xFFFFFFFFu, next_have);
+        next_block = P.pages + (static_cast<uint64_t>(next_have ? id : 0) * P.kv_heads + static_cast<uint32_t>(ahead.head)) *
+                                   P.block.bytes;
+    };
+    auto issue = [&](bool v) {
+        split_issue<D, ES>(P, next_block, v, next_have, next_pages, (ahead.q.c_lo + ahead.c) & 1, lane,
+                           v ? S.v[warp] : S.k[warp], v ? &S.v_full[warp] : &S.k_full[warp]);
+    };
+    seek(warp);
+    bool pending_k = false, pending_v = false, dead = false;
+    if (next) {
+        take_pages();
+        issue(false);
+        issue(true);
+        pending_k = pending_v = true;
+    }
+    uint32_t pages = next_pages;
+    bool have_chunk = next;
+    if (next) seek(kSplitWarps);
 
-    int64_t x = x0;
-    bool dead = false;
     SplitUnit<D> U;
     while (x < x1) {
-        const int n = static_cast<int>(min(static_cast<int64_t>(seg.q.chunks - seg.c), x1 - x));  // the share's chunks of this unit
+        const int n = static_cast<int>(min(static_cast<int64_t>(seg.q.chunks - seg.c), x1 - x));
         const bool whole_unit = n == seg.q.chunks;
-        // the warp's own chunks of it
         const bool mine_any = cx < x + n;
         if (mine_any) {
             split_load_unit<D>(P, seg, lane, U);
             for (; cx < x + n; cx += kSplitWarps) {
-                const uint32_t st = used % kSplitStages;
-                uint32_t pages = have[0];
-#pragma unroll
-                for (int i = 1; i < kSplitStages; ++i)
-                    if (st == static_cast<uint32_t>(i)) pages = have[i];
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.full[warp][st], used / kSplitStages & 1u, dead ? 0 : P.wait_ns))) {
-                    err |= DF11_DEV_ERR_TIMEOUT;
-                    dead = true;
-                    pages = 0;
-                }
-                ++used;
-                split_chunk<D>(P, S.ring[warp][st], (seg.q.c_lo + seg.c + (cx - x)) * static_cast<int64_t>(kSplitKeys), pages, lane, U);
+                const int key0 = (seg.q.c_lo + seg.c + static_cast<int>(cx - x)) * kSplitKeys;
+                auto wait = [&](uint64_t *bar) {
+                    if (!have_chunk || !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, dead ? 0 : P.wait_ns))) {
+                        err |= DF11_DEV_ERR_TIMEOUT;
+                        dead = true;
+                        pages = 0;
+                    }
+                };
+                wait(&S.k_full[warp]);
+                pending_k = dead && pending_k;
+                bool whole = pages == (1u << (kSplitKeys >> ES)) - 1u && key0 >= U.all_lo && key0 + kSplitKeys <= U.all_hi;
+                float s[4][4];
+                split_scores<D, ES>(S.k[warp], key0, pages, whole, lane, U, s);
                 __syncwarp();
-                if (ax < x1 && !dead) {
-                    if (lane < 16) fence_proxy_async_smem();
-                    __syncwarp();
-                    issue();
+                const bool more = next && !dead;
+                if (more) {
+                    fence_proxy_async_smem();
+                    take_pages();
+                    issue(false);
+                    pending_k = true;
                 }
+                uint32_t pb[4][2];
+                split_softmax<D>(s, U, pb);
+                wait(&S.v_full[warp]);
+                pending_v = dead && pending_v;
+                whole = whole && !dead;
+                split_values<D, ES>(S.v[warp], key0, pages, whole, lane, U, pb);
+                __syncwarp();
+                if (more && !dead) {
+                    fence_proxy_async_smem();
+                    issue(true);
+                    pending_v = true;
+                }
+                have_chunk = more;
+                pages = next_pages;
+                parity ^= 1u;
+                if (more) seek(kSplitWarps);
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -644,6 +708,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
         for (int it = tid; it < kSplitCols * D / 4; it += kSplitThreads) {
             const int col = it / (D / 4), d = it % (D / 4) * 4;
             float m = -INFINITY, l = 0.0f;
+#pragma unroll
             for (int w = 0; w < kSplitWarps; ++w) m = fmaxf(m, S.m[w][col]);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int w = 0; w < kSplitWarps; ++w) {
@@ -679,8 +744,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
                     const int col = it / (D / 4), d = it % (D / 4) * 4;
                     float m = -INFINITY, l = 0.0f;
 #pragma unroll 4
-                    for (int c = first_cta; c <= last_cta; ++c)
-                        m = fmaxf(m, __ldcg(part(c) + kSplitCols * D + col));
+                    for (int c = first_cta; c <= last_cta; ++c) m = fmaxf(m, __ldcg(part(c) + kSplitCols * D + col));
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                     for (int c = first_cta; c <= last_cta; ++c) {
@@ -697,11 +761,16 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
             }
         }
         x += n;
-        if (x < x1) seg.advance(P, n);
-        __syncthreads();
+        if (x < x1) {
+            seg.advance(P, n);
+            __syncthreads();
+        }
     }
     // after a timeout: the copies still out must land before the memory is given up
-    for (; dead && used < issued; ++used) mbar_wait(&S.full[warp][used % kSplitStages], used / kSplitStages & 1u, P.wait_ns);
+    if (dead) {
+        if (pending_k) mbar_wait(&S.k_full[warp], parity, P.wait_ns);
+        if (pending_v) mbar_wait(&S.v_full[warp], parity, P.wait_ns);
+    }
     report(P.err, __reduce_or_sync(0xFFFFFFFFu, err) * (lane == 0));
 }
 
@@ -1286,6 +1355,16 @@ AttnParams attn_params(const df11_kv4_cache &c, const df11_kv4_attention_args &a
 }
 
 template <int D>
+void launch_split(const AttnParams &P, int ctas, cudaStream_t s) {
+    constexpr size_t smem = sizeof(SplitShared<D>);
+    switch (P.page_shift) {
+        case 4: attention_split_kernel<D, 4><<<ctas, kSplitThreads, smem, s>>>(P); break;
+        case 5: attention_split_kernel<D, 5><<<ctas, kSplitThreads, smem, s>>>(P); break;
+        default: attention_split_kernel<D, 6><<<ctas, kSplitThreads, smem, s>>>(P); break;
+    }
+}
+
+template <int D>
 constexpr size_t kPrefillSmem = sizeof(PrefillShared<D>) + 1024;  // and what aligns it
 
 bool prepare(int *sms) {
@@ -1302,8 +1381,12 @@ bool prepare(int *sms) {
             return cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
         };
-        if (!allow(&attention_split_kernel<64>, sizeof(SplitShared<64>)) ||
-            !allow(&attention_split_kernel<128>, sizeof(SplitShared<128>)) ||
+        if (!allow(&attention_split_kernel<64, 4>, sizeof(SplitShared<64>)) ||
+            !allow(&attention_split_kernel<64, 5>, sizeof(SplitShared<64>)) ||
+            !allow(&attention_split_kernel<64, 6>, sizeof(SplitShared<64>)) ||
+            !allow(&attention_split_kernel<128, 4>, sizeof(SplitShared<128>)) ||
+            !allow(&attention_split_kernel<128, 5>, sizeof(SplitShared<128>)) ||
+            !allow(&attention_split_kernel<128, 6>, sizeof(SplitShared<128>)) ||
             !allow(&attention_prefill_kernel<64>, kPrefillSmem<64>) ||
             !allow(&attention_prefill_kernel<128>, kPrefillSmem<128>))
             return false;
@@ -1326,8 +1409,8 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
     const AttnParams P = attn_params(c, a, err);
     int sms = 0;
     if (!prepare(&sms)) return LaunchStatus::kCuda;
-    if (c.head_dim == 128) attention_split_kernel<128><<<sms, kSplitThreads, sizeof(SplitShared<128>), s>>>(P);
-    else attention_split_kernel<64><<<sms, kSplitThreads, sizeof(SplitShared<64>), s>>>(P);
+    if (c.head_dim == 128) launch_split<128>(P, sms, s);
+    else launch_split<64>(P, sms, s);
     if (static_cast<int64_t>(a.max_q_len) * P.group > kSplitMaxRows) {
         // as many pairs of tiles as the rows can make: full ones, and a last
         // one of each request that has more rows than the other path takes
