@@ -44,23 +44,10 @@ constexpr int kSplitWarps = 12;
 constexpr int kSplitThreads = 32 * kSplitWarps;
 constexpr int kSplitCols = 8;      // rows of a unit
 constexpr int kSplitKeys = 64;     // keys of a chunk: a warp's step
+constexpr int kSplitStages = 2;    // chunks that a warp has room for
 constexpr int kSplitMaxRows = 64;  // rows (tokens x heads of a group) of a request that go this way
 constexpr int kSplitAlign = 4 * kSplitWarps;  // units of at most so many chunks are not shared between CTAs
 constexpr int32_t kMaxKeys = INT32_MAX - 255;
-
-template <int D>
-struct SplitShared {
-    static constexpr uint32_t kHalf = kSplitKeys * D * 9 / 16;  // K or V of a chunk
-    static constexpr int kPitch = D + 4;  // floats; spreads a thread's columns over the banks
-    alignas(128) uint8_t k[kSplitWarps][kHalf], v[kSplitWarps][kHalf];
-    alignas(16) float o[kSplitWarps][kSplitCols][kPitch];
-    float m[kSplitWarps][kSplitCols], l[kSplitWarps][kSplitCols];
-    alignas(8) uint64_t k_full[kSplitWarps], v_full[kSplitWarps];
-    int64_t sums[kSplitWarps];
-    int64_t start_off, end;
-    int32_t longest[kSplitWarps];
-    int32_t start_req, last;
-};
 
 // A partial result in the workspace: unnormalised O (8 x D), then m and l.
 template <int D>
@@ -132,6 +119,44 @@ struct SplitPos {
     __device__ __forceinline__ int key0() const { return (q.c_lo + c) * kSplitKeys; }
 };
 
+// Keys that every row of a unit sees [all_lo, all_hi), and that any does [any_lo, any_hi).
+struct SplitSeen {
+    int all_lo, all_hi, any_lo, any_hi;
+};
+
+__device__ __forceinline__ SplitSeen split_seen(const AttnParams &P, const SplitPos &at) {
+    const int group = static_cast<int>(P.group), base = at.q.kv - at.q.n;
+    const int p0 = base + at.tile * kSplitCols / group;  // rows ascend
+    const int p1 = base + (min((at.tile + 1) * kSplitCols, at.q.rows) - 1) / group;
+    SplitSeen s;
+    s.all_hi = P.a.causal ? min(p0 + 1, at.q.end) : at.q.end;
+    s.any_hi = P.a.causal ? min(p1 + 1, at.q.end) : at.q.end;
+    s.all_lo = P.a.window ? p1 + 1 - P.a.window : 0;
+    s.any_lo = P.a.window ? max(p0 + 1 - P.a.window, 0) : 0;
+    return s;
+}
+
+// Where a warp leaves its result of a unit for others: O (8 x kSplitPitch
+// floats, which spreads a thread's columns over the banks), then m and l.
+template <int D>
+constexpr int kSplitPitch = D + 4;
+
+template <int D>
+struct SplitShared {
+    static constexpr uint32_t kStage = kSplitKeys * D * 9 / 8;  // a chunk's K and V
+    static constexpr uint32_t kResult = 4 * (kSplitCols * kSplitPitch<D> + 2 * kSplitCols);
+    static_assert(kResult <= kStage, "a result fits the stage of a chunk");
+    alignas(128) uint8_t ring[kSplitWarps][kSplitStages][kStage];
+    alignas(8) uint64_t full[kSplitWarps][kSplitStages];
+    SplitPos pos[kSplitWarps][kSplitStages];  // of the chunk in a stage
+    SplitSeen seen[kSplitWarps];
+    int ready[kSplitWarps];  // 2 x the segment (its end in the share) whose result is in a stage, + the stage
+    int freed[kSplitWarps];  // the last one that was taken from there
+    SplitPos last_pos, join_pos[2];
+    int join_first[2], join_last[2], join[2];
+    int dead;  // a wait gave up: what the CTA has is not joined
+};
+
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
@@ -152,6 +177,17 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// log(sum exp) from a maximum in log2 units and the sum relative to it: -inf
+// where no key was seen (l is 0), NaN where a score was.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -160,12 +196,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 // What a warp has of a unit: its queries as the B operand, and per column
 // (the thread's are 2t and 2t + 1) the factor of the scores (log2 units), the
-// keys seen, the running maximum and sum, and O.
+// token's position, the running maximum and sum, and O.
 template <int D>
 struct SplitUnit {
     uint32_t qb[D / 16][2];
     float f[2], m[2], l[2];
-    int lo[2], hi[2], all_lo, all_hi, any_lo, any_hi;
+    int pos[2];  // key position of the column's token
     float o[D / 16][4];
 };
 
@@ -219,22 +255,8 @@ __device__ __forceinline__ void split_load_unit(const AttnParams &P, const Split
         U.f[i] = A.scale * P.k_scale * 1.44269504088896341f * __uint_as_float(static_cast<uint32_t>(ec + 127) << 23);
         U.m[i] = -INFINITY;
         U.l[i] = 0.0f;
-        const int rc = tile * kSplitCols + col;
-        U.lo[i] = 0;
-        U.hi[i] = INT32_MAX;
-        if (rc < at.q.rows) {
-            const int pos = base + rc / group;
-            if (A.causal) U.hi[i] = pos + 1;
-            if (A.window) U.lo[i] = pos + 1 - A.window;
-        }
+        U.pos[i] = base + min(tile * kSplitCols + col, at.q.rows - 1) / group;
     }
-    // what every row of the tile sees, and what any does (rows ascend)
-    const int p0 = base + tile * kSplitCols / group;
-    const int p1 = base + (min((tile + 1) * kSplitCols, at.q.rows) - 1) / group;
-    U.all_hi = A.causal ? min(p0 + 1, at.q.end) : at.q.end;
-    U.any_hi = A.causal ? min(p1 + 1, at.q.end) : at.q.end;
-    U.all_lo = A.window ? p1 + 1 - A.window : 0;
-    U.any_lo = A.window ? max(p0 + 1 - A.window, 0) : 0;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -253,33 +275,36 @@ __device__ __forceinline__ int64_t split_page(const AttnParams &P, const SplitPo
     return __ldg(P.a.block_table + static_cast<int64_t>(at.r) * P.a.max_pages + pg);
 }
 
-// Copies the K (or V) halves of a chunk's pages, of the unit's head, into
-// shared memory, each as the half of a block of 2^ES tokens.
+// Copies a chunk's pages, of the unit's head, into a stage, each as a block of 2^ES tokens.
 template <int D, int ES>
-__device__ __forceinline__ void split_issue(const AttnParams &P, const uint8_t *block, bool v, bool have, uint32_t mask,
-                                            int half, int lane, uint8_t *dst, uint64_t *bar) {
+__device__ __forceinline__ void split_issue(const AttnParams &P, const uint8_t *block, bool have, uint32_t mask, int half,
+                                            int lane, uint8_t *dst, uint64_t *bar) {
     constexpr Kv4Block B = kv4_block(1u << ES, D);
     if (ES < 6 || P.page_shift == 6) {
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * B.v_codes);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * B.bytes);
         __syncwarp();
-        if (have) bulk_load(dst + lane * B.v_codes, block + (v ? B.v_codes : 0u), B.v_codes, bar);
+        if (have) bulk_load(dst + lane * B.bytes, block, B.bytes, bar);
     } else {
         // half of a 128-token page: its rows of the row-ordered sections are
         // contiguous, the V scales are 64 bytes of each element block's 128
-        if (lane == 0) mbar_arrive_expect_tx(bar, mask ? B.v_codes : 0u);
+        if (lane == 0) mbar_arrive_expect_tx(bar, mask ? B.bytes : 0u);
         const uint8_t *s = reinterpret_cast<const uint8_t *>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(block), 0));
         constexpr uint32_t codes = B.k_scales, scales = B.v_codes - B.k_scales;
-        if (mask && lane == 0) bulk_load(dst, s + (v ? P.block.v_codes : 0u) + half * codes, codes, bar);
-        if (mask && lane == 1 && !v) bulk_load(dst + codes, s + P.block.k_scales + half * scales, scales, bar);
-        if (mask && v && lane >= 1 && lane < 1 + D / 16)
-            bulk_load(dst + codes + (lane - 1) * 64, s + P.block.v_scales + (lane - 1) * 128 + half * 64, 64, bar);
+        if (mask) {
+            if (lane == 0) bulk_load(dst, s + half * codes, codes, bar);
+            if (lane == 1) bulk_load(dst + B.k_scales, s + P.block.k_scales + half * scales, scales, bar);
+            if (lane == 2) bulk_load(dst + B.v_codes, s + P.block.v_codes + half * codes, codes, bar);
+            if (lane >= 3 && lane < 3 + D / 16)
+                bulk_load(dst + B.v_scales + (lane - 3) * 64, s + P.block.v_scales + (lane - 3) * 128 + half * 64, 64, bar);
+        }
     }
 }
 
 // The scores of a chunk's 64 keys, in log2 units; what a row does not see is -inf.
 template <int D, int ES>
-__device__ __forceinline__ void split_scores(const uint8_t *stage, int key0, uint32_t pages, bool whole, int lane,
-                                             const SplitUnit<D> &U, float (&s)[4][4]) {
+__device__ __forceinline__ void split_scores(const AttnParams &P, const uint8_t *stage, int key0, uint32_t pages,
+                                             bool whole, const SplitSeen &seen, int lane, const SplitUnit<D> &U,
+                                             float (&s)[4][4]) {
     constexpr int KW = D / 32;  // words of a thread's K codes of one key
     constexpr Kv4Block B = kv4_block(1u << ES, D);
     const int g = lane >> 2, t = lane & 3;
@@ -299,8 +324,8 @@ __device__ __forceinline__ void split_scores(const uint8_t *stage, int key0, uin
             const uint32_t page = (16u * (i + z)) >> ES, off = (16u * (i + z)) & ((1u << ES) - 1u);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const uint8_t *c = codes + page * B.v_codes + (off + 2u * r) * (D / 2);
-                const uint8_t *x = scales + page * B.v_codes + (off + 2u * r) * (D / 16);
+                const uint8_t *c = codes + page * B.bytes + (off + 2u * r) * (D / 2);
+                const uint8_t *x = scales + page * B.bytes + (off + 2u * r) * (D / 16);
                 if constexpr (D == 128) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(c);
                     w[z][r][0] = v.x, w[z][r][1] = v.y, w[z][r][2] = v.z, w[z][r][3] = v.w;
@@ -343,7 +368,8 @@ __device__ __forceinline__ void split_scores(const uint8_t *stage, int key0, uin
             for (int x = 0; x < 4; ++x) {
                 const uint32_t in = 16u * i + kg + (x & 2u);
                 const int key = key0 + static_cast<int>(in);
-                if (!(pages >> (in >> ES) & 1u) || key < U.lo[x & 1] || key >= U.hi[x & 1] || key >= U.any_hi)
+                if (!(pages >> (in >> ES) & 1u) || key >= seen.any_hi || (P.a.causal && key > U.pos[x & 1]) ||
+                    (P.a.window && key <= U.pos[x & 1] - P.a.window))
                     s[i][x] = -INFINITY;
             }
     }
@@ -392,25 +418,26 @@ __device__ __forceinline__ void split_softmax(float (&s)[4][4], SplitUnit<D> &U,
 
 // O^T += V^T P^T over the chunk's keys.
 template <int D, int ES>
-__device__ __forceinline__ void split_values(const uint8_t *stage, int key0, uint32_t pages, bool whole, int lane,
-                                             SplitUnit<D> &U, const uint32_t (&pb)[4][2]) {
+__device__ __forceinline__ void split_values(const uint8_t *stage, int key0, uint32_t pages, bool whole,
+                                             const SplitSeen &seen, int lane, SplitUnit<D> &U,
+                                             const uint32_t (&pb)[4][2]) {
     constexpr Kv4Block B = kv4_block(1u << ES, D);
     const int g = lane >> 2, t = lane & 3;
     const int b = D == 128 ? g : g >> 1;  // the scale block of the thread's elements [g D / 8, (g + 1) D / 8)
-    const uint8_t *codes = stage + (t * (D / 16) + b) * 32;
-    const uint8_t *scales = stage + B.k_scales + (b << ES) + 4 * t;
+    const uint8_t *codes = stage + B.v_codes + (t * (D / 16) + b) * 32;
+    const uint8_t *scales = stage + B.v_scales + (b << ES) + 4 * t;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t in = 16u * i, page = in >> ES, off = in & ((1u << ES) - 1u);
-        const uint8_t *c = codes + page * B.v_codes + (off >> 2) * (D / 16) * 32u;
-        uint32_t vs = *reinterpret_cast<const uint32_t *>(scales + page * B.v_codes + off);
+        const uint8_t *c = codes + page * B.bytes + (off >> 2) * (D / 16) * 32u;
+        uint32_t vs = *reinterpret_cast<const uint32_t *>(scales + page * B.bytes + off);
         if (!whole) {
             // a key that no row sees may hold anything, NaN scales too: 0 times NaN must not reach a sum
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const uint32_t k = in + 4 * t + x;
                 const int key = key0 + static_cast<int>(k);
-                if (!(pages >> (k >> ES) & 1u) || key < U.any_lo || key >= U.any_hi) vs &= ~(0xFFu << (8 * x));
+                if (!(pages >> (k >> ES) & 1u) || key < seen.any_lo || key >= seen.any_hi) vs &= ~(0xFFu << (8 * x));
             }
         }
         const uint32_t sc[2] = {e4m3x2_to_f16x2(vs & 0xFFFFu), e4m3x2_to_f16x2(vs >> 16)};
@@ -446,37 +473,90 @@ __device__ __forceinline__ void split_values(const uint8_t *stage, int key0, uin
     }
 }
 
-// Four elements of a finished row.
-template <int D>
-__device__ __forceinline__ void split_store(const AttnParams &P, const SplitPos &at, int col, int d, float4 o, float m,
+// Elements [d, d + N) of a finished row.
+template <int D, int N>
+__device__ __forceinline__ void split_store(const AttnParams &P, const SplitPos &at, int col, int d, const float *o, float m,
                                             float l) {
     const df11_kv4_attention_args &A = P.a;
     const int row = at.tile * kSplitCols + col, group = static_cast<int>(P.group);
     if (row >= at.q.rows) return;
     const int64_t token = at.q.q0 + row / group;
     const int hq = at.head * group + row % group;
-    const float s = l > 0.0f ? P.v_scale / l : 0.0f;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * s, o.y * s), b = __floats2bfloat162_rn(o.z * s, o.w * s);
-    uint2 w;
-    w.x = *reinterpret_cast<const uint32_t *>(&a);
-    w.y = *reinterpret_cast<const uint32_t *>(&b);
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.o) + token * static_cast<int64_t>(A.o_token_stride) + hq * D + d) =
-        w;
-    if (A.lse && d == 0)
-        A.lse[token * A.n_q_heads + hq] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    const float s = l > 0.0f ? P.v_scale / l : l;  // 0 where no key was seen
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = bf16x2_of(o[2 * i] * s, o[2 * i + 1] * s);
+    uint16_t *p = static_cast<uint16_t *>(A.o) + token * static_cast<int64_t>(A.o_token_stride) + hq * D + d;
+    if constexpr (N == 4) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 4)
+            *reinterpret_cast<uint4 *>(p + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+    if (A.lse && d == 0) A.lse[token * A.n_q_heads + hq] = lse_of(m, l);
+}
+
+// CTA b's share of the launch's chunks starts here: equal parts, the first total % ctas one longer.
+struct SplitShares {
+    int base, rem;
+    __device__ __forceinline__ int start(int b) const { return b * base + min(b, rem); }
+    // The CTA that has chunk y.
+    __device__ __forceinline__ int owner(int y) const {
+        const int longer = rem * (base + 1);
+        return y < longer ? y / (base + 1) : rem + (y - longer) / base;
+    }
+};
+
+// Waits until every lane's flag word (null: none), but for the bits `loose`,
+// holds `want`; false after limit_ns, which sets *dead, or when *dead is set.
+__device__ __forceinline__ bool flags_wait(const int *flag, int want, int loose, int *dead, uint64_t limit_ns) {
+    auto there = [&]() {
+        return __all_sync(0xFFFFFFFFu, !flag || (*reinterpret_cast<const volatile int *>(flag) & ~loose) == want) != 0;
+    };
+    bool ok = there();
+    if (!ok) {
+        const uint64_t t0 = global_ns();
+        while (!(ok = there())) {
+            const bool late = global_ns() - t0 > limit_ns;
+            if (late) atomicExch(dead, 1);
+            if (__any_sync(0xFFFFFFFFu, late || *reinterpret_cast<volatile int *>(dead))) break;
+        }
+    }
+    __threadfence_block();
+    return ok;
+}
+
+// A thread's part of a warp's result: columns 2t and 2t + 1, elements [g D / 8, (g + 1) D / 8).
+template <int D>
+__device__ __forceinline__ void split_put(float *at, int lane, const SplitUnit<D> &U) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        float *o = at + (2 * t + c) * kSplitPitch<D> + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 2)
+            *reinterpret_cast<float4 *>(o + 2 * i) = make_float4(U.o[i][c], U.o[i][2 + c], U.o[i + 1][c], U.o[i + 1][2 + c]);
+        if (g == 0) {
+            at[kSplitCols * kSplitPitch<D> + 2 * t + c] = U.m[c];
+            at[kSplitCols * kSplitPitch<D> + kSplitCols + 2 * t + c] = U.l[c];
+        }
+    }
 }
 
 // Persistent CTAs, each a contiguous, equal share of the launch's chunks
 // (request, unit, chunk in order), so a long request spreads over the GPU and
 // short ones share a CTA, whatever the mix.  A share's chunks go to the warps
-// in turn; each warp has room for one chunk in shared memory, and refills its
-// K half as soon as the scores are taken and its V half after the second
-// product, with the next chunk, across unit ends.  At the end of a unit (or of
-// the share) the warps' results are joined in shared memory; a unit that spans
-// CTAs goes through the workspace, and the CTA that arrives last joins its
-// parts in order: no CTA waits for another, and the result does not depend on
-// which one was last.  Where all units are short (kSplitAlign), a unit goes to
-// the CTA that has its first chunk: fewer CTAs, but no join between them.
+// in turn, and the warps run on their own, each with a ring of two chunks that
+// its own copies fill, across unit ends.  A unit's part in a share is a
+// segment.  Within the share, a warp leaves its result of a segment in the
+// stage it has just used and goes on; the warp with the segment's last chunk
+// joins them.  The share's last segment is joined by the whole CTA.  A unit
+// that spans CTAs goes through the workspace, and the CTA that arrives last
+// joins its parts at its own end, in order: no CTA waits for another, and the
+// result does not depend on which one was last.  Where all units are short
+// (kSplitAlign), a unit goes whole to the CTA whose share holds its first
+// chunk: fewer CTAs work, but none joins.
 template <int D, int ES>
 __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -485,291 +565,357 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t err = 0;
     if (lane == 0) {
-        mbar_init(&S.k_full[warp], 1);
-        mbar_init(&S.v_full[warp], 1);
+#pragma unroll
+        for (int i = 0; i < kSplitStages; ++i) mbar_init(&S.full[warp][i], 1);
         fence_mbar_init();
+        S.ready[warp] = S.freed[warp] = -1;
+        if (warp < 2) S.join[warp] = 0;
+        if (warp == 0) S.dead = 0;
     }
 
-    // ---- the launch's chunks, and the request in which this CTA's share starts
-    int64_t mine = 0;
-    int longest = 0;
-    const int room = key_room(P);
-    for (int r = tid; r < A.n_reqs; r += kSplitThreads) {
+    // ---- the launch's chunks (the host has seen that they fit 31 bits);
+    // every warp counts them by itself, so none waits
+    int total = 0, longest = 0;
+    for (int r = lane; r < A.n_reqs; r += 32) {
         const SplitReq q = split_req(P, r);
-        mine += static_cast<int64_t>(q.units) * q.chunks;
+        total += q.units * q.chunks;
         if (q.units) longest = max(longest, q.chunks);
-        if (blockIdx.x == 0) {
+        if (blockIdx.x == 0 && warp == 0) {
             if (!rows_valid(A, __ldg(A.q_start + r), __ldg(A.q_start + r + 1))) err |= DF11_DEV_ERR_AUX;
-            if (__ldg(A.kv_lens + r) > room) err |= DF11_DEV_ERR_PAGES;
+            if (__ldg(A.kv_lens + r) > key_room(P)) err |= DF11_DEV_ERR_PAGES;
         }
     }
-    const int longest_mine = longest;  // with a thread per request, that request's chunks
-    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-    if (lane == 0) S.longest[warp] = longest;
-    auto block_scan = [&](int64_t v, int64_t &all) -> int64_t {  // exclusive
-        int64_t incl = v;
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, x);
-            if (lane >= x) incl += o;
-        }
-        __syncthreads();
-        if (lane == 31) S.sums[warp] = incl;
-        __syncthreads();
-        int64_t before = 0;
-        all = 0;
-#pragma unroll
-        for (int w = 0; w < kSplitWarps; ++w) {
-            if (w < warp) before += S.sums[w];
-            all += S.sums[w];
-        }
-        return before + incl - v;
-    };
-    int64_t total;
-    const int64_t at0 = block_scan(mine, total);
-#pragma unroll
-    for (int w = 0; w < kSplitWarps; ++w) longest = max(longest, S.longest[w]);
-    const bool aligned = longest <= kSplitAlign;
+    total = static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(total)));
+    const bool aligned = __reduce_max_sync(0xFFFFFFFFu, longest) <= kSplitAlign;
+    __syncthreads();
     // no share is empty: a unit's parts are then those of every CTA from its first to its last
-    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
-    if (blockIdx.x >= ctas) {
+    const int ctas = min(static_cast<int>(gridDim.x), total);
+    if (static_cast<int>(blockIdx.x) >= ctas) {
         report(P.err, err);
         return;
     }
-    int64_t x0 = total * blockIdx.x / ctas, x1 = total * (blockIdx.x + 1) / ctas;
-    // a request that holds the share's first or (aligned) last position, its chunks from `at` on, says where in it that is
-    auto place = [&](int r, int64_t at, int64_t weight, int chunks) {
-        if (!weight) return;
-        if (at <= x0 && x0 < at + weight) {
-            S.start_req = r;
-            S.start_off = x0 - at;
-        }
-        if (aligned && at < x1 && x1 < at + weight) S.end = at + (x1 - at + chunks - 1) / chunks * chunks;
-    };
-    if (tid == 0) S.end = x1;
-    if (A.n_reqs <= kSplitThreads) {
-        __syncthreads();
-        place(tid, at0, mine, longest_mine);
-    } else {
-        int64_t base = 0;
-        for (int b = 0; b < A.n_reqs && base <= x1; b += kSplitThreads) {
-            int64_t v = 0, all;
-            int chunks = 1;
-            if (b + tid < A.n_reqs) {
-                const SplitReq q = split_req(P, b + tid);
-                v = static_cast<int64_t>(q.units) * q.chunks;
-                chunks = q.chunks;
-            }
-            const int64_t at = base + block_scan(v, all);
-            place(b + tid, at, v, chunks);
-            base += all;
-        }
-    }
-    __syncthreads();
-    SplitPos seg;  // the unit being computed, at the share's first chunk of it
-    seg.r = S.start_req;
-    seg.q = split_req(P, seg.r);
+    const SplitShares shares{total / ctas, total % ctas};
+    int x0 = shares.start(blockIdx.x), x1 = shares.start(blockIdx.x + 1);
+    // ---- the share's start as a position; an aligned share's ends moved to the next unit starts
+    SplitPos ahead;  // of this warp's next chunk to copy
     {
-        const int64_t off = S.start_off;
-        const int unit = static_cast<int>(off / seg.q.chunks);
-        seg.head = unit / seg.q.tiles;
-        seg.tile = unit % seg.q.tiles;
-        seg.c = static_cast<int>(off % seg.q.chunks);
-    }
-    if (aligned) {
-        x1 = S.end;
-        if (seg.c) {
-            const int skip = seg.q.chunks - seg.c;
+        int base = 0, off = 0, end = x1, req = 0;
+        for (int b = 0; b < A.n_reqs && base <= x1; b += 32) {
+            SplitReq q{};
+            if (b + lane < A.n_reqs) q = split_req(P, b + lane);
+            const int w = q.units * q.chunks;
+            int incl = w;
+#pragma unroll
+            for (int y = 1; y < 32; y <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, incl, y);
+                if (lane >= y) incl += o;
+            }
+            const int at = base + incl - w;
+            const uint32_t holds0 = __ballot_sync(0xFFFFFFFFu, w && at <= x0 && x0 < at + w);
+            const uint32_t holds1 = __ballot_sync(0xFFFFFFFFu, w && at < x1 && x1 < at + w);
+            if (holds0) {
+                const int src = __ffs(holds0) - 1;
+                req = b + src;
+                off = __shfl_sync(0xFFFFFFFFu, x0 - at, src);
+            }
+            if (holds1 && aligned) {
+                const int chunks = max(q.chunks, 1);
+                end = __shfl_sync(0xFFFFFFFFu, at + (x1 - at + chunks - 1) / chunks * chunks, __ffs(holds1) - 1);
+            }
+            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        ahead.r = req;
+        ahead.q = split_req(P, req);
+        const int unit = off / ahead.q.chunks;
+        ahead.head = unit / ahead.q.tiles;
+        ahead.tile = unit % ahead.q.tiles;
+        ahead.c = off - unit * ahead.q.chunks;
+        x1 = end;
+        if (aligned && ahead.c) {
+            const int skip = ahead.q.chunks - ahead.c;
             x0 += skip;
-            if (x0 < x1) seg.advance(P, skip);
+            if (x0 < x1) ahead.advance(P, skip);
         }
         if (x0 >= x1) {
             report(P.err, err);
             return;
         }
     }
+    const int share = x1 - x0;  // indexes from here on count from the share's first chunk
 
-    // ---- this warp's copies, one chunk ahead of its computation
-    SplitPos ahead = seg;
-    int64_t ax = x0, cx = x0 + warp, x = x0;  // the launch's index of ahead, of this warp's next chunk, of seg
+    // ---- this warp's copies, up to two chunks ahead of its computation
+    int ax = 0;         // index of `ahead`
     bool next = false;  // there is a chunk at `ahead` for this warp
-    uint32_t next_pages = 0, parity = 0;
-    const uint8_t *next_block = nullptr;
-    bool next_have = false;
+    uint32_t pages[kSplitStages] = {};
     int64_t id = kNoPage;
     auto seek = [&](int by) {
         ax += by;
-        next = ax < x1;
+        next = ax < share;
         if (next) {
             ahead.advance(P, by);
             id = split_page<ES>(P, ahead, lane);
         }
     };
-    auto take_pages = [&]() {
-        next_have = id >= 0 && static_cast<uint64_t>(id) < P.n_pages;
-        if (!next_have && id != kNoPage) err |= DF11_DEV_ERR_PAGES;
-        next_pages = __ballot_sync(0xFFFFFFFFu, next_have);
-        next_block = P.pages + (static_cast<uint64_t>(next_have ? id : 0) * P.kv_heads + static_cast<uint32_t>(ahead.head)) *
-                                   P.block.bytes;
-    };
-    auto issue = [&](bool v) {
-        split_issue<D, ES>(P, next_block, v, next_have, next_pages, (ahead.q.c_lo + ahead.c) & 1, lane,
-                           v ? S.v[warp] : S.k[warp], v ? &S.v_full[warp] : &S.k_full[warp]);
+    // copies the chunk at `ahead` into stage st and moves on to the one after
+    int issued = 0, landed = 0;
+    auto issue = [&](int st) {
+        ++issued;
+        if (lane == 0) S.pos[warp][st] = ahead;
+        const bool have = id >= 0 && static_cast<uint64_t>(id) < P.n_pages;
+        if (!have && id != kNoPage) err |= DF11_DEV_ERR_PAGES;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, have);
+        const uint8_t *block = P.pages + (static_cast<uint64_t>(have ? id : 0) * P.kv_heads +
+                                          static_cast<uint32_t>(ahead.head)) * P.block.bytes;
+        split_issue<D, ES>(P, block, have, mask, (ahead.q.c_lo + ahead.c) & 1, lane, S.ring[warp][st], &S.full[warp][st]);
+        if (st) pages[1] = mask;
+        else pages[0] = mask;
+        seek(kSplitWarps);
     };
     seek(warp);
-    bool pending_k = false, pending_v = false, dead = false;
-    if (next) {
-        take_pages();
-        issue(false);
-        issue(true);
-        pending_k = pending_v = true;
-    }
-    uint32_t pages = next_pages;
-    bool have_chunk = next;
-    if (next) seek(kSplitWarps);
+#pragma unroll 1
+    for (int i = 0; i < kSplitStages && next; ++i) issue(i);
 
     SplitUnit<D> U;
-    while (x < x1) {
-        const int n = static_cast<int>(min(static_cast<int64_t>(seg.q.chunks - seg.c), x1 - x));
-        const bool whole_unit = n == seg.q.chunks;
-        const bool mine_any = cx < x + n;
-        if (mine_any) {
-            split_load_unit<D>(P, seg, lane, U);
-            for (; cx < x + n; cx += kSplitWarps) {
-                const int key0 = (seg.q.c_lo + seg.c + static_cast<int>(cx - x)) * kSplitKeys;
-                auto wait = [&](uint64_t *bar) {
-                    if (!have_chunk || !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, dead ? 0 : P.wait_ns))) {
-                        err |= DF11_DEV_ERR_TIMEOUT;
-                        dead = true;
-                        pages = 0;
-                    }
-                };
-                wait(&S.k_full[warp]);
-                pending_k = dead && pending_k;
-                bool whole = pages == (1u << (kSplitKeys >> ES)) - 1u && key0 >= U.all_lo && key0 + kSplitKeys <= U.all_hi;
-                float s[4][4];
-                split_scores<D, ES>(S.k[warp], key0, pages, whole, lane, U, s);
+    bool dead = false;   // a wait gave up: no more copies
+    int held = -1;       // the segment whose result is in the stage that the next copy goes to
+    bool in_last = false;  // U is this warp's part of the share's last segment
+    for (int cx = warp, st = 0, parity = 0, s0 = 0, s1 = 0; cx < share; cx += kSplitWarps) {
+        const SplitPos &at = S.pos[warp][st];
+        __syncwarp();
+        if (cx >= s1) {
+            s0 = max(cx - at.c, 0);
+            s1 = min(cx - at.c + at.q.chunks, share);
+            if (lane == 0) S.seen[warp] = split_seen(P, at);
+            split_load_unit<D>(P, at, lane, U);
+            __syncwarp();
+        }
+        const int key0 = at.key0();
+        const SplitSeen &seen = S.seen[warp];
+        uint8_t *stage = S.ring[warp][st];
+        uint32_t there = st ? pages[1] : pages[0];
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.full[warp][st], parity, P.wait_ns))) {
+            err |= DF11_DEV_ERR_TIMEOUT;
+            dead = true;
+            there = 0;
+            if (lane == 0) atomicExch(&S.dead, 1);
+            mbar_wait(&S.full[warp][st], parity, P.wait_ns);  // the memory is not given up with a copy on its way
+        }
+        ++landed;
+        const bool whole = there == (1u << (kSplitKeys >> ES)) - 1u && key0 >= seen.all_lo && key0 + kSplitKeys <= seen.all_hi;
+        float s[4][4];
+        split_scores<D, ES>(P, stage, key0, there, whole, seen, lane, U, s);
+        uint32_t pb[4][2];
+        split_softmax<D>(s, U, pb);
+        split_values<D, ES>(stage, key0, there, whole, seen, lane, U, pb);
+        __syncwarp();
+        // the other stage, if a result was in it until now: taken by now, as a
+        // rule, and waited for before this warp leaves another
+        if (held >= 0 && !dead) {
+            if (!flags_wait(lane == 0 ? &S.freed[warp] : nullptr, held, 0, &S.dead, P.wait_ns)) {
+                err |= DF11_DEV_ERR_TIMEOUT;
+                dead = true;
+            } else if (next) {
+                fence_proxy_async_smem();
                 __syncwarp();
-                const bool more = next && !dead;
-                if (more) {
-                    fence_proxy_async_smem();
-                    take_pages();
-                    issue(false);
-                    pending_k = true;
-                }
-                uint32_t pb[4][2];
-                split_softmax<D>(s, U, pb);
-                wait(&S.v_full[warp]);
-                pending_v = dead && pending_v;
-                whole = whole && !dead;
-                split_values<D, ES>(S.v[warp], key0, pages, whole, lane, U, pb);
-                __syncwarp();
-                if (more && !dead) {
-                    fence_proxy_async_smem();
-                    issue(true);
-                    pending_v = true;
-                }
-                have_chunk = more;
-                pages = next_pages;
-                parity ^= 1u;
-                if (more) seek(kSplitWarps);
+                issue(st ^ 1);
             }
+        }
+        held = -1;
+        bool keep = false;  // the stage holds a result
+        if (cx + kSplitWarps >= s1) {
+            // ---- the end of the segment [s0, s1) for this warp
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int y = 4; y < 32; y <<= 1) U.l[c] += __shfl_xor_sync(0xFFFFFFFFu, U.l[c], y);
-        }
-        // ---- join: the warps' results in shared memory
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (g == 0) {
-                S.m[warp][2 * t + c] = mine_any ? U.m[c] : -INFINITY;
-                S.l[warp][2 * t + c] = mine_any ? U.l[c] : 0.0f;
-            }
-            if (mine_any) {
-                float *o = &S.o[warp][2 * t + c][g * (D / 8)];
-#pragma unroll
-                for (int i = 0; i < D / 16; i += 2)
-                    *reinterpret_cast<float4 *>(o + 2 * i) =
-                        make_float4(U.o[i][c], U.o[i][2 + c], U.o[i + 1][c], U.o[i + 1][2 + c]);
-            }
-        }
-        __syncthreads();
-        // parts of a unit that spans CTAs: CTAs first_cta .. last_cta, each one part
-        const int64_t u0 = x - seg.c, u1 = u0 + seg.q.chunks;
-        auto owner = [&](int64_t y) { return static_cast<int>(((y + 1) * ctas + total - 1) / total - 1); };
-        const int first_cta = whole_unit ? 0 : owner(u0), last_cta = whole_unit ? 0 : owner(u1 - 1);
-        // a CTA has at most two parts: of the unit that its share starts inside (0), and of the one it ends inside (1)
-        auto part = [&](int cta) {
-            return static_cast<float *>(A.workspace) + P.ws_parts +
-                   (2ull * cta + (cta == first_cta ? 1 : 0)) * split_partial_floats<D>();
-        };
-        for (int it = tid; it < kSplitCols * D / 4; it += kSplitThreads) {
-            const int col = it / (D / 4), d = it % (D / 4) * 4;
-            float m = -INFINITY, l = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kSplitWarps; ++w) m = fmaxf(m, S.m[w][col]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < kSplitWarps; ++w) {
-                if (S.m[w][col] == -INFINITY) continue;
-                const float f = ex2(S.m[w][col] - m);
-                const float4 v = *reinterpret_cast<const float4 *>(&S.o[w][col][d]);
-                o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
-                l += f * S.l[w][col];
-            }
-            if (whole_unit) {
-                split_store<D>(P, seg, col, d, o, m, l);
+            if (s1 == share) {
+                in_last = true;
+                if (lane == 0 && cx == share - 1) S.last_pos = at;
+            } else if (cx != s1 - 1) {
+                split_put<D>(reinterpret_cast<float *>(stage), lane, U);
+                __threadfence_block();
+                __syncwarp();
+                if (lane == 0) *reinterpret_cast<volatile int *>(&S.ready[warp]) = 2 * s1 + st;
+                keep = true;
             } else {
-                float *p = part(blockIdx.x);
-                __stcg(reinterpret_cast<float4 *>(p + col * D + d), o);
-                if (d == 0) {
-                    __stcg(p + kSplitCols * D + col, m);
-                    __stcg(p + kSplitCols * D + kSplitCols + col, l);
+                // join: this warp's result is in registers; lane i looks at the segment's i-th warp
+                const int warps = min(s1 - s0, kSplitWarps), g = lane >> 2, t = lane & 3;
+                const int mate = (s0 + lane) % kSplitWarps;
+                const bool other = lane < warps && mate != warp;
+                if (!flags_wait(other ? &S.ready[mate] : nullptr, 2 * s1, 1, &S.dead, P.wait_ns)) {
+                    err |= DF11_DEV_ERR_TIMEOUT;
+                    dead = true;
                 }
-            }
-        }
-        if (!whole_unit) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                int *counter = static_cast<int *>(A.workspace) + first_cta;
-                S.last = atomicAdd(counter, 1) == last_cta - first_cta;
-                if (S.last) *counter = 0;
-            }
-            __syncthreads();
-            if (S.last) {
-                __threadfence();
-                for (int it = tid; it < kSplitCols * D / 4; it += kSplitThreads) {
-                    const int col = it / (D / 4), d = it % (D / 4) * 4;
-                    float m = -INFINITY, l = 0.0f;
-#pragma unroll 4
-                    for (int c = first_cta; c <= last_cta; ++c) m = fmaxf(m, __ldcg(part(c) + kSplitCols * D + col));
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = first_cta; c <= last_cta; ++c) {
-                        const float *p = part(c);
-                        const float mc = __ldcg(p + kSplitCols * D + col);
-                        const float lc = __ldcg(p + kSplitCols * D + kSplitCols + col);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + col * D + d));
-                        const float f = mc == -INFINITY ? 0.0f : ex2(mc - m);
-                        o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
-                        l += f * lc;
+                for (int i = 0; i < warps; ++i) {
+                    const int w = (s0 + i) % kSplitWarps;
+                    if (w == warp) continue;
+                    const float *r = reinterpret_cast<const float *>(S.ring[w][S.ready[w] & 1]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float mw = r[kSplitCols * kSplitPitch<D> + 2 * t + c], mn = fmaxf(U.m[c], mw);
+                        const float sh = mn == -INFINITY ? 0.0f : mn, f = ex2(U.m[c] - sh), h = ex2(mw - sh);
+                        U.m[c] = mn;
+                        U.l[c] = U.l[c] * f + h * r[kSplitCols * kSplitPitch<D> + kSplitCols + 2 * t + c];
+                        const float *o = r + (2 * t + c) * kSplitPitch<D> + g * (D / 8);
+#pragma unroll
+                        for (int y = 0; y < D / 16; y += 2) {
+                            const float4 v = *reinterpret_cast<const float4 *>(o + 2 * y);
+                            U.o[y][c] = U.o[y][c] * f + h * v.x, U.o[y][2 + c] = U.o[y][2 + c] * f + h * v.y;
+                            U.o[y + 1][c] = U.o[y + 1][c] * f + h * v.z, U.o[y + 1][2 + c] = U.o[y + 1][2 + c] * f + h * v.w;
+                        }
                     }
-                    split_store<D>(P, seg, col, d, o, m, l);
+                }
+                __threadfence_block();
+                __syncwarp();
+                if (other) *reinterpret_cast<volatile int *>(&S.freed[mate]) = s1;
+                if (s1 - s0 == at.q.chunks) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float o[D / 8];
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) o[2 * i] = U.o[i][c], o[2 * i + 1] = U.o[i][2 + c];
+                        split_store<D, D / 8>(P, at, 2 * t + c, g * (D / 8), o, U.m[c], U.l[c]);
+                    }
+                } else {
+                    // the share starts inside this unit: its part, of those of CTAs first .. last (this one)
+                    const int first = shares.owner(x0 + cx - at.c), last = blockIdx.x;
+                    float *p = static_cast<float *>(A.workspace) + P.ws_parts +
+                               2ull * blockIdx.x * split_partial_floats<D>();
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int i = 0; i < D / 16; i += 2)
+                            __stcg(reinterpret_cast<float4 *>(p + (2 * t + c) * D + g * (D / 8) + 2 * i),
+                                   make_float4(U.o[i][c], U.o[i][2 + c], U.o[i + 1][c], U.o[i + 1][2 + c]));
+                        if (g == 0) {
+                            __stcg(p + kSplitCols * D + 2 * t + c, U.m[c]);
+                            __stcg(p + kSplitCols * D + kSplitCols + 2 * t + c, U.l[c]);
+                        }
+                    }
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) {
+                        int *counter = static_cast<int *>(A.workspace) + first;
+                        if (atomicAdd(counter, 1) == last - first) {
+                            *counter = 0;
+                            __threadfence();
+                            S.join_pos[0] = at;
+                            S.join_first[0] = first;
+                            S.join_last[0] = last;
+                            S.join[0] = 1;
+                        }
+                    }
                 }
             }
         }
-        x += n;
-        if (x < x1) {
-            seg.advance(P, n);
-            __syncthreads();
+        if (keep) {
+            held = s1;
+        } else if (next && !dead) {
+            fence_proxy_async_smem();
+            issue(st);
+        }
+        if (dead) {
+            // the rest of the share is given up, but for the copy that may still be out
+            if (issued > landed) mbar_wait(&S.full[warp][st ^ 1], parity ^ st, P.wait_ns);
+            break;
+        }
+        st ^= 1;
+        if (!st) parity ^= 1;
+    }
+
+    // ---- the share's last segment, joined by the CTA
+    __syncthreads();
+    if (S.dead) {
+        report(P.err, __reduce_or_sync(0xFFFFFFFFu, err) * (lane == 0));
+        return;
+    }
+    float *results = reinterpret_cast<float *>(&S.ring[0][0][0]);
+    constexpr int kResult = SplitShared<D>::kResult / 4;
+    const SplitPos last = S.last_pos;
+    const int n_last = min(last.c + 1, share), s0 = share - n_last;  // its chunks of the share: from s0 on
+    const int warps = min(n_last, kSplitWarps);
+    if (in_last) split_put<D>(results + warp * kResult, lane, U);
+    __syncthreads();
+    const bool whole_unit = n_last == last.q.chunks;
+    const int u0 = x0 + share - 1 - last.c;
+    const int first = whole_unit ? 0 : shares.owner(u0), final = whole_unit ? 0 : shares.owner(u0 + last.q.chunks - 1);
+    // a CTA's parts: of the unit that its share starts inside (0), and of the one that goes on in the next CTA's (1)
+    auto part = [&](int cta, int first_cta) {
+        return static_cast<float *>(A.workspace) + P.ws_parts +
+               (2ull * cta + (cta == first_cta ? 1 : 0)) * split_partial_floats<D>();
+    };
+    for (int it = tid; it < kSplitCols * D / 4; it += kSplitThreads) {
+        const int col = it / (D / 4), d = it % (D / 4) * 4;
+        float m = -INFINITY, l = 0.0f, o[4] = {};
+        for (int i = 0; i < warps; ++i) m = fmaxf(m, results[(s0 + i) % kSplitWarps * kResult + kSplitCols * kSplitPitch<D> + col]);
+        const float sh = m == -INFINITY ? 0.0f : m;
+#pragma unroll 4
+        for (int i = 0; i < warps; ++i) {
+            const float *r = results + (s0 + i) % kSplitWarps * kResult;
+            const float h = ex2(r[kSplitCols * kSplitPitch<D> + col] - sh);
+            const float4 v = *reinterpret_cast<const float4 *>(r + col * kSplitPitch<D> + d);
+            l += h * r[kSplitCols * kSplitPitch<D> + kSplitCols + col];
+            o[0] += h * v.x, o[1] += h * v.y, o[2] += h * v.z, o[3] += h * v.w;
+        }
+        if (whole_unit) {
+            split_store<D, 4>(P, last, col, d, o, m, l);
+        } else {
+            float *p = part(blockIdx.x, first);
+            __stcg(reinterpret_cast<float4 *>(p + col * D + d), make_float4(o[0], o[1], o[2], o[3]));
+            if (d == 0) {
+                __stcg(p + kSplitCols * D + col, m);
+                __stcg(p + kSplitCols * D + kSplitCols + col, l);
+            }
         }
     }
-    // after a timeout: the copies still out must land before the memory is given up
-    if (dead) {
-        if (pending_k) mbar_wait(&S.k_full[warp], parity, P.wait_ns);
-        if (pending_v) mbar_wait(&S.v_full[warp], parity, P.wait_ns);
+    if (!whole_unit) {
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();  // the CTA's stores, seen at the barrier, before the arrival
+            int *counter = static_cast<int *>(A.workspace) + first;
+            if (atomicAdd(counter, 1) == final - first) {
+                *counter = 0;
+                __threadfence();
+                S.join_pos[1] = last;
+                S.join_first[1] = first;
+                S.join_last[1] = final;
+                S.join[1] = 1;
+            }
+        }
+    }
+    // ---- units whose last part was this CTA's
+    __syncthreads();
+    for (int kind = 0; kind < 2; ++kind) {
+        if (!S.join[kind]) continue;
+        const int b0 = S.join_first[kind], b1 = S.join_last[kind];
+        for (int it = tid; it < kSplitCols * D / 4; it += kSplitThreads) {
+            const int col = it / (D / 4), d = it % (D / 4) * 4;
+            float m = -INFINITY, l = 0.0f, o[4] = {};
+            for (int b = b0; b <= b1; b += 8) {
+                float mb[8], lb[8];
+                float4 ob[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float *p = part(min(b + i, b1), b0);
+                    mb[i] = b + i > b1 ? -INFINITY : __ldcg(p + kSplitCols * D + col);
+                    lb[i] = __ldcg(p + kSplitCols * D + kSplitCols + col);
+                    ob[i] = __ldcg(reinterpret_cast<const float4 *>(p + col * D + d));
+                }
+                float top = m;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, mb[i]);
+                const float sh = top == -INFINITY ? 0.0f : top, f = ex2(m - sh);
+                m = top;
+                l *= f, o[0] *= f, o[1] *= f, o[2] *= f, o[3] *= f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float h = ex2(mb[i] - sh);
+                    l += lb[i] * h;
+                    o[0] += ob[i].x * h, o[1] += ob[i].y * h, o[2] += ob[i].z * h, o[3] += ob[i].w * h;
+                }
+            }
+            split_store<D, 4>(P, S.join_pos[kind], col, d, o, m, l);
+        }
     }
     report(P.err, __reduce_or_sync(0xFFFFFFFFu, err) * (lane == 0));
 }
@@ -891,11 +1037,6 @@ __device__ __forceinline__ PrefillWork prefill_work(const AttnParams &P, int req
         W.a1[x] = e[x] > b[x] ? static_cast<int32_t>(e[x] - first) : 0;
     }
     return W;
-}
-
-__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&p);
 }
 
 // The block-table entry of key `key`, or kNoPage where the page holds no key a row sees.
@@ -1114,7 +1255,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
             tc_fence_after();
         }
         if (!run) err |= DF11_DEV_ERR_TIMEOUT;
-        const float inv = run && l > 0.0f ? P.v_scale / l : 0.0f;
+        const float inv = !run ? 0.0f : l > 0.0f ? P.v_scale / l : l;  // NaN stays NaN
         uint16_t *op = static_cast<uint16_t *>(A.o) + token * static_cast<int64_t>(A.o_token_stride) + hq * D;
 #pragma unroll
         for (int i = 0; i < D; i += 16) {
@@ -1139,7 +1280,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
                 }
             }
         }
-        if (live && A.lse) A.lse[token * A.n_q_heads + hq] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (live && A.lse) A.lse[token * A.n_q_heads + hq] = lse_of(m, l);
         tc_fence_before();
     } else if (warp < 12) {
         // =============================== the cache to FP16 operand tiles
@@ -1408,6 +1549,10 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
                                   cudaStream_t s) {
     const AttnParams P = attn_params(c, a, err);
     int sms = 0;
+    // the split path counts chunks in 31 bits
+    const int64_t tiles = (std::min<int64_t>(static_cast<int64_t>(a.max_q_len) * P.group, kSplitMaxRows) + kSplitCols - 1) / kSplitCols;
+    const int64_t chunks = std::max<int64_t>(((static_cast<int64_t>(a.max_pages) << P.page_shift) + kSplitKeys - 1) / kSplitKeys, 1);
+    if (static_cast<double>(a.n_reqs) * P.kv_heads * tiles * chunks >= 2147483648.0) return LaunchStatus::kUnsupported;
     if (!prepare(&sms)) return LaunchStatus::kCuda;
     if (c.head_dim == 128) launch_split<128>(P, sms, s);
     else launch_split<64>(P, sms, s);

@@ -782,7 +782,8 @@ typedef struct {
     float scale;                /* of the scores, finite */
     void *workspace;            /* df11_kv4_attention_workspace_bytes, 16-byte aligned; all zero before its
                                    first use, after which every call leaves what the next one needs.
-                                   Calls that may run at the same time need one each */
+                                   Calls that may run at the same time need one each; zero it again
+                                   after DF11_DEV_ERR_TIMEOUT */
     uint64_t workspace_bytes;
 } df11_kv4_attention_args;
 
@@ -803,8 +804,9 @@ uint64_t df11_kv4_attention_workspace_bytes(const df11_kv4_cache *cache, const d
  * max_pages * page_size (those keys are left out).  DF11_DEV_ERR_AUX:
  * q_start descending or past n_tokens, or a request longer than max_q_len
  * (those rows are not written).
- * Errors: DF11_EINVAL, DF11_EUNSUPPORTED (head_dim or page_size), DF11_ENOMEM
- * (workspace too small), DF11_ECUDA. */
+ * Errors: DF11_EINVAL, DF11_EUNSUPPORTED (head_dim, page_size, or a call of
+ * 2^31 or more chunks of 64 keys, counted over the cache's heads and max_pages
+ * for every request: split it), DF11_ENOMEM (workspace too small), DF11_ECUDA. */
 df11_status df11_kv4_attention(const df11_kv4_cache *cache, const df11_kv4_attention_args *args, int *dev_err_flag,
                                df11_stream stream);
 

@@ -488,6 +488,23 @@ def test_many_requests(df11, n):
     p.check(o, lse)
 
 
+@pytest.mark.parametrize("hq,h,d,page", [(8, 8, 64, 16), (8, 4, 128, 64), (4, 4, 64, 128)])
+def test_long_batches(df11, hq, h, d, page):
+    """Shares of several long units, and of long beside very short ones: a warp's results of one unit after another
+    are joined by other warps while it goes on."""
+    g = np.random.default_rng(page)
+    lens = [(1, int(x)) for x in g.integers(800, 4200, 48)]
+    lens[5:5] = [(1, 3), (1, 0), (1, 64), (1, 65)] * 3
+    lens[40:40] = [(1, 1)] * 30
+    p = Problem(df11, lens, hq, h, d, page, seed=page)
+    o, lse, err = p.run()
+    assert err.item() == 0
+    p.check(o, lse)
+    for _ in range(3):
+        o2, lse2, err = p.run(ws=p.keep[-1])
+        assert err.item() == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_score_ranges(df11, n):
     """Scores far apart (one key takes all), tiny and huge queries and keys, a scale of 0 and a negative one."""
