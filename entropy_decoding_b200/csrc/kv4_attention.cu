@@ -1420,51 +1420,67 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
     } else {
         // =============================== MMAs
         asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-        if (warp == 12 && lane == 0 && W.steps) {
+        // the whole warp walks, so that addresses and descriptors stay uniform;
+        // one elected lane issues
+        if (warp == 12 && W.steps) {
             // FP32 accumulate, FP16 A and B, M = 128; N = keys of a step, then head elements
             constexpr uint32_t idesc_s = (1u << 4) | ((kPrefillTile >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t idesc_o = (1u << 4) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
+            const bool leader = elect_one();
             bool run = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                run = run && __all_sync(0xFFFFFFFFu, prefill_wait(bar, parity, S, P.wait_ns));
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (leader) tc_commit(bar);
+                __syncwarp();
+            };
             auto scores = [&](int x, int j) {
-                if (j == W.a0[x]) run = run && prefill_wait(&S.q_full[x], 0, S, P.wait_ns);
+                if (j == W.a0[x]) wait(&S.q_full[x], 0);
                 if (!run) return;
                 tc_fence_after();
-                const uint32_t q = smem_addr(S.q[x]), k = smem_addr(S.k[j & 1]);
+                const uint64_t q = swz128_desc(smem_addr(S.q[x])), k = swz128_desc(smem_addr(S.k[j & 1]));
+                if (leader) {
 #pragma unroll
-                for (uint32_t i = 0; i < D / 16; ++i) {
-                    const uint32_t at = (i / 4) * (kPrefillTile * 128) + (i % 4) * 32;
-                    tc_mma(tmem + x * kPrefillTile, swz128_desc(q + at), swz128_desc(k + at), idesc_s, i > 0);
+                    for (uint32_t i = 0; i < D / 16; ++i) {
+                        const uint32_t at = ((i / 4) * (kPrefillTile * 128) + (i % 4) * 32) >> 4;
+                        tc_mma(tmem + x * kPrefillTile, q + at, k + at, idesc_s, i > 0);
+                    }
                 }
-                tc_commit(&S.s_full[x]);
+                __syncwarp();
+                commit(&S.s_full[x]);
             };
             auto values = [&](int x, int j) {
-                run = run && prefill_wait(&S.v_full[j & 1], (j >> 1) & 1u, S, P.wait_ns) &&
-                      prefill_wait(&S.p_full[x], (j - W.a0[x]) & 1u, S, P.wait_ns);
+                wait(&S.v_full[j & 1], (j >> 1) & 1u);
+                wait(&S.p_full[x], (j - W.a0[x]) & 1u);
                 if (!run) return;
                 tc_fence_after();
-                const uint32_t v = smem_addr(S.v[j & 1]);
+                const uint64_t v = swz128_desc(smem_addr(S.v[j & 1]));
+                const uint32_t more = j > W.a0[x];
+                if (leader) {
 #pragma unroll
-                for (uint32_t i = 0; i < kPrefillTile / 16; ++i)
-                    tc_mma_ts(tmem + 2 * kPrefillTile + x * D, tmem + x * kPrefillTile + i * 8,
-                              swz128_desc(v + (i / 4) * (D * 128) + (i % 4) * 32), idesc_o, i > 0 || j > W.a0[x]);
-                tc_commit(&S.o_done[x]);
+                    for (uint32_t i = 0; i < kPrefillTile / 16; ++i)
+                        tc_mma_ts(tmem + 2 * kPrefillTile + x * D, tmem + x * kPrefillTile + i * 8,
+                                  v + (((i / 4) * (D * 128) + (i % 4) * 32) >> 4), idesc_o, i > 0 ? 1u : more);
+                }
+                __syncwarp();
+                commit(&S.o_done[x]);
             };
             auto active = [&](int x, int j) { return j >= W.a0[x] && j < W.a1[x]; };
             for (int j = 0; j < W.steps && run; ++j) {
-                run = prefill_wait(&S.k_full[j & 1], (j >> 1) & 1u, S, P.wait_ns);
+                wait(&S.k_full[j & 1], (j >> 1) & 1u);
                 if (run && active(0, j)) scores(0, j);
                 if (run && j && active(1, j - 1)) values(1, j - 1);
-                if (run && j) tc_commit(&S.v_empty[(j - 1) & 1]);
+                if (run && j) commit(&S.v_empty[(j - 1) & 1]);
                 if (run && active(1, j)) scores(1, j);
-                if (run) tc_commit(&S.k_empty[j & 1]);
+                if (run) commit(&S.k_empty[j & 1]);
                 if (run && active(0, j)) values(0, j);
             }
             if (run && active(1, W.steps - 1)) values(1, W.steps - 1);
             // every MMA has completed before the CTA ends
-            tc_commit(&S.end);
-            if (!mbar_wait(&S.end, 0, P.wait_ns) || !run) err |= DF11_DEV_ERR_TIMEOUT;
+            commit(&S.end);
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.end, 0, P.wait_ns)) || !run) err |= DF11_DEV_ERR_TIMEOUT;
         }
-        __syncwarp();
     }
     err = __reduce_or_sync(0xFFFFFFFFu, err);
     if (lane == 0) report(P.err, err);
