@@ -188,6 +188,34 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two floats in a register pair, and the instructions that take such pairs.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ float low(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float high(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -944,9 +972,10 @@ constexpr float kLazy = 8.0f;      // log2 units a row's maximum may grow before
 template <int D>
 struct PrefillShared {
     static constexpr uint32_t kOperand = kPrefillTile * D * 2;
+    static constexpr uint32_t kQ = 0, kK = 2 * kOperand, kV = 4 * kOperand;  // offsets of q, k, v
     alignas(1024) uint8_t q[2][kOperand];
     uint8_t k[2][kOperand], v[2][kOperand];
-    uint32_t ok[4][4];  // keys of a step that are there; the softmax may read a step's while the next two are decoded
+    alignas(16) uint32_t ok[4][4];  // keys of a step that are there; the softmax may read a step's while the next two are decoded
     uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], end;
     int32_t sums[kPrefillThreads / 32];
     uint32_t tmem, abort;
@@ -959,10 +988,13 @@ __device__ __forceinline__ uint32_t swz_chunk(uint32_t row, uint32_t chunk) {
     return row * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
-// Shared-memory matrix descriptor of such a tile (K-major, 8-row groups 1024 bytes apart).
-__device__ __forceinline__ uint64_t swz128_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (uint64_t{1} << 16) | (uint64_t{1024 >> 4} << 32) |
-           (uint64_t{1} << 46) | (uint64_t{2} << 61);
+// Shared-memory matrix descriptor of such a tile (K-major, 8-row groups 1024
+// bytes apart): the low word from its address, to which multiples of 16 bytes
+// may be added as units, and the whole from the low word.
+__device__ __forceinline__ uint32_t swz128_desc_low(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+
+__device__ __forceinline__ uint64_t swz128_desc(uint32_t low) {
+    return static_cast<uint64_t>(low) | (static_cast<uint64_t>((1024u >> 4) | (1u << 14) | (2u << 29)) << 32);
 }
 
 template <class Shared>
@@ -1117,7 +1149,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
 
     if (warp < 8) {
         // =============================== softmax of tile x, a thread per row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int x = warp >> 2, r = tid & 127;
         const int row = W.row0 + x * kPrefillTile + r;
         const bool live = row < W.rows;
@@ -1164,48 +1196,52 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
             fence_proxy_async_smem();
             mbar_arrive(&S.q_full[x]);
         }
-        int64_t lo = 0, hi = 0;
-        if (live) prefill_row(P, W, row, lo, hi);
+        // keys [lo, hi) seen by this row, from the tile's first step on
+        int lo = 0, hi = 0;
+        if (live) {
+            int64_t lo64, hi64;
+            prefill_row(P, W, row, lo64, hi64);
+            const int64_t from = static_cast<int64_t>(W.first + W.a0[x]) * kPrefillTile;
+            lo = static_cast<int>(max(lo64 - from, static_cast<int64_t>(0)));
+            hi = static_cast<int>(max(hi64 - from, static_cast<int64_t>(0)));
+        }
         float m = -INFINITY, l = 0.0f;
         bool run = true;
         for (int it = 0; it < steps; ++it) {
             const int j = W.a0[x] + it;
-            const int64_t key0 = static_cast<int64_t>(W.first + j) * kPrefillTile;
             run = __all_sync(0xFFFFFFFFu, prefill_wait(&S.s_full[x], it & 1u, S, P.wait_ns));
             if (!run) break;
             tc_fence_after();
             uint32_t s[kPrefillTile];
 #pragma unroll
             for (int i = 0; i < 4; ++i) tc_ld32(s_col + 32 * i, s + 32 * i);
-            // keys [a, b) of the step seen by this row
-            const int a = static_cast<int>(min(max(lo - key0, static_cast<int64_t>(0)), static_cast<int64_t>(kPrefillTile)));
-            const int b = static_cast<int>(min(max(hi - key0, static_cast<int64_t>(0)), static_cast<int64_t>(kPrefillTile)));
-            uint32_t seen[4];
-            bool full = true;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int ai = min(max(a - 32 * i, 0), 32), bi = min(max(b - 32 * i, 0), 32);
-                const uint32_t below = bi == 32 ? 0xFFFFFFFFu : (1u << bi) - 1u;
-                seen[i] = (ai == 32 ? 0u : below & (0xFFFFFFFFu << ai)) &
-                          *reinterpret_cast<volatile uint32_t *>(&S.ok[j & 3][i]);
-                full &= seen[i] == 0xFFFFFFFFu;
-            }
+            uint4 ok;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(ok.x), "=r"(ok.y), "=r"(ok.z), "=r"(ok.w)
+                         : "r"(smem_addr(S.ok[j & 3]))
+                         : "memory");
             tc_wait_ld();
+            const int left = hi - it * kPrefillTile, right = lo - it * kPrefillTile;
+            const bool full = left >= kPrefillTile && right <= 0 && (ok.x & ok.y & ok.z & ok.w) == 0xFFFFFFFFu;
             if (__any_sync(0xFFFFFFFFu, !full)) {
+                const uint32_t words[4] = {ok.x, ok.y, ok.z, ok.w};
 #pragma unroll
-                for (int i = 0; i < kPrefillTile; ++i)
-                    if (!(seen[i / 32] >> (i % 32) & 1u)) s[i] = 0xFF800000u;  // -inf
-            }
-            float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[1]), t2 = __uint_as_float(s[2]),
-                  t3 = __uint_as_float(s[3]);
+                for (int i = 0; i < 4; ++i) {
+                    const int ai = min(max(right - 32 * i, 0), 32), bi = min(max(left - 32 * i, 0), 32);
+                    const uint32_t below = bi == 32 ? 0xFFFFFFFFu : (1u << bi) - 1u;
+                    const uint32_t seen = ai == 32 ? 0u : words[i] & below & (0xFFFFFFFFu << ai);
 #pragma unroll
-            for (int i = 4; i < kPrefillTile; i += 4) {
-                t0 = fmaxf(t0, __uint_as_float(s[i]));
-                t1 = fmaxf(t1, __uint_as_float(s[i + 1]));
-                t2 = fmaxf(t2, __uint_as_float(s[i + 2]));
-                t3 = fmaxf(t3, __uint_as_float(s[i + 3]));
+                    for (int y = 0; y < 32; ++y)
+                        if (!(seen >> y & 1u)) s[32 * i + y] = 0xFF800000u;  // -inf
+                }
             }
-            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+            float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[1]);
+#pragma unroll
+            for (int i = 2; i < kPrefillTile - 2; i += 4) {
+                t0 = max3(t0, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                t1 = max3(t1, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+            }
+            const float top = max3(fmaxf(t0, t1), __uint_as_float(s[kPrefillTile - 2]), __uint_as_float(s[kPrefillTile - 1]));
             const float mt = top == -INFINITY ? -INFINITY : top * f;
             const bool grow = mt > m + kLazy || (m == -INFINITY && mt != -INFINITY);
             if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -1229,23 +1265,23 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
                 }
             }
             const float shift = m == -INFINITY ? 0.0f : m;
-            float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
+            // two at a time: p = 2^(s f - shift), and their sums
+            const uint64_t f2 = pair(f, f), shift2 = pair(-shift, -shift);
+            uint64_t la = 0, lb = 0;
 #pragma unroll
             for (int c = 0; c < kPrefillTile; c += 32) {
                 uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float p0 = ex2(fmaf(__uint_as_float(s[c + i]), f, -shift));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[c + i + 1]), f, -shift));
-                    const float p2 = ex2(fmaf(__uint_as_float(s[c + i + 2]), f, -shift));
-                    const float p3 = ex2(fmaf(__uint_as_float(s[c + i + 3]), f, -shift));
-                    l0 += p0, l1 += p1, l2 += p2, l3 += p3;
-                    w[i / 2] = pack_f16(p0, p1);
-                    w[i / 2 + 1] = pack_f16(p2, p3);
+                for (int i = 0; i < 16; ++i) {
+                    const uint64_t e = fma2(pair(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])), f2, shift2);
+                    const float p0 = ex2(low(e)), p1 = ex2(high(e));
+                    (i & 1 ? lb : la) = add2(i & 1 ? lb : la, pair(p0, p1));
+                    w[i] = pack_f16(p0, p1);
                 }
                 tc_st16(s_col + c / 2, w);
             }
-            l += (l0 + l1) + (l2 + l3);
+            la = add2(la, lb);
+            l += low(la) + high(la);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(&S.p_full[x]);
@@ -1284,7 +1320,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
         tc_fence_before();
     } else if (warp < 12) {
         // =============================== the cache to FP16 operand tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         constexpr uint32_t NB = D / 16;
         const int u = tid - 256;  // K: the step's key; V: 8 keys and 16 elements
         const int unit = u >> 3;  // V: 16 chunks of 8 keys x NB blocks, lanes of 8 over the chunks of one 128-byte row
@@ -1419,68 +1455,76 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
         }
     } else {
         // =============================== MMAs
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-        // the whole warp walks, so that addresses and descriptors stay uniform;
-        // one elected lane issues
-        if (warp == 12 && W.steps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        // one elected lane walks: the instructions between a wait and the MMAs it
+        // holds back are on the critical path, so descriptors are made once and
+        // the steps go in pairs, whose stages are then constants
+        if (warp == 12 && W.steps && elect_one()) {
             // FP32 accumulate, FP16 A and B, M = 128; N = keys of a step, then head elements
             constexpr uint32_t idesc_s = (1u << 4) | ((kPrefillTile >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t idesc_o = (1u << 4) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
-            const bool leader = elect_one();
+            using Sh = PrefillShared<D>;
+            // low words of the descriptors: the shared block's address (in 16
+            // bytes) and a constant; `here` keeps the sums from being made
+            // ahead of the loop, in registers that this role does not have
+            auto here = [](uint32_t v) {
+                asm volatile("" : "+r"(v));
+                return v;
+            };
+            const uint32_t base = swz128_desc_low(smem_addr(&S));
+            const int a0[2] = {W.a0[0], W.a0[1]}, a1[2] = {W.a1[0], W.a1[1]}, steps = W.steps;
             bool run = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                run = run && __all_sync(0xFFFFFFFFu, prefill_wait(bar, parity, S, P.wait_ns));
-            };
-            auto commit = [&](uint64_t *bar) {
-                if (leader) tc_commit(bar);
-                __syncwarp();
-            };
-            auto scores = [&](int x, int j) {
-                if (j == W.a0[x]) wait(&S.q_full[x], 0);
+            uint32_t parity = 0;  // of both stages' phases in this pair of steps
+            auto wait = [&](uint64_t *bar, uint32_t ph) { run = run && prefill_wait(bar, ph, S, P.wait_ns); };
+            // x, st: constants where this is inlined
+            auto scores = [&](int x, int st, int j) {
+                if (j == a0[x]) wait(&S.q_full[x], 0);
                 if (!run) return;
                 tc_fence_after();
-                const uint64_t q = swz128_desc(smem_addr(S.q[x])), k = swz128_desc(smem_addr(S.k[j & 1]));
-                if (leader) {
+                const uint32_t b = here(base);
 #pragma unroll
-                    for (uint32_t i = 0; i < D / 16; ++i) {
-                        const uint32_t at = ((i / 4) * (kPrefillTile * 128) + (i % 4) * 32) >> 4;
-                        tc_mma(tmem + x * kPrefillTile, q + at, k + at, idesc_s, i > 0);
-                    }
+                for (uint32_t i = 0; i < D / 16; ++i) {
+                    const uint32_t at = (i / 4) * (kPrefillTile * 128) + (i % 4) * 32;
+                    tc_mma(tmem + x * kPrefillTile, swz128_desc(b + ((Sh::kQ + x * Sh::kOperand + at) >> 4)),
+                           swz128_desc(b + ((Sh::kK + st * Sh::kOperand + at) >> 4)), idesc_s, i > 0);
                 }
-                __syncwarp();
-                commit(&S.s_full[x]);
+                tc_commit(&S.s_full[x]);
             };
-            auto values = [&](int x, int j) {
-                wait(&S.v_full[j & 1], (j >> 1) & 1u);
-                wait(&S.p_full[x], (j - W.a0[x]) & 1u);
+            auto values = [&](int x, int st, uint32_t ph, int j) {
+                wait(&S.v_full[st], ph);
+                wait(&S.p_full[x], (j - a0[x]) & 1u);
                 if (!run) return;
                 tc_fence_after();
-                const uint64_t v = swz128_desc(smem_addr(S.v[j & 1]));
-                const uint32_t more = j > W.a0[x];
-                if (leader) {
+                const uint32_t more = j > a0[x], b = here(base);
 #pragma unroll
-                    for (uint32_t i = 0; i < kPrefillTile / 16; ++i)
-                        tc_mma_ts(tmem + 2 * kPrefillTile + x * D, tmem + x * kPrefillTile + i * 8,
-                                  v + (((i / 4) * (D * 128) + (i % 4) * 32) >> 4), idesc_o, i > 0 ? 1u : more);
-                }
-                __syncwarp();
-                commit(&S.o_done[x]);
+                for (uint32_t i = 0; i < kPrefillTile / 16; ++i)
+                    tc_mma_ts(tmem + 2 * kPrefillTile + x * D, tmem + x * kPrefillTile + i * 8,
+                              swz128_desc(b + ((Sh::kV + st * Sh::kOperand + (i / 4) * (D * 128) + (i % 4) * 32) >> 4)),
+                              idesc_o, i > 0 ? 1u : more);
+                tc_commit(&S.o_done[x]);
             };
-            auto active = [&](int x, int j) { return j >= W.a0[x] && j < W.a1[x]; };
-            for (int j = 0; j < W.steps && run; ++j) {
-                wait(&S.k_full[j & 1], (j >> 1) & 1u);
-                if (run && active(0, j)) scores(0, j);
-                if (run && j && active(1, j - 1)) values(1, j - 1);
-                if (run && j) commit(&S.v_empty[(j - 1) & 1]);
-                if (run && active(1, j)) scores(1, j);
-                if (run) commit(&S.k_empty[j & 1]);
-                if (run && active(0, j)) values(0, j);
+            auto active = [&](int x, int j) { return j >= a0[x] && j < a1[x]; };
+            auto step = [&](int st, int j) {
+                wait(&S.k_full[st], parity);
+                if (run && active(0, j)) scores(0, st, j);
+                if (run && j) {
+                    if (active(1, j - 1)) values(1, st ^ 1, st ? parity : parity ^ 1u, j - 1);
+                    if (run) tc_commit(&S.v_empty[st ^ 1]);
+                }
+                if (run && active(1, j)) scores(1, st, j);
+                if (run) tc_commit(&S.k_empty[st]);
+                if (run && active(0, j)) values(0, st, parity, j);
+            };
+            for (int j = 0; j < steps && run; j += 2, parity ^= 1u) {
+                step(0, j);
+                if (run && j + 1 < steps) step(1, j + 1);
             }
-            if (run && active(1, W.steps - 1)) values(1, W.steps - 1);
+            if (run && active(1, steps - 1)) values(1, (steps - 1) & 1, ((steps - 1) >> 1) & 1u, steps - 1);
             // every MMA has completed before the CTA ends
-            commit(&S.end);
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.end, 0, P.wait_ns)) || !run) err |= DF11_DEV_ERR_TIMEOUT;
+            tc_commit(&S.end);
+            if (!mbar_wait(&S.end, 0, P.wait_ns) || !run) err |= DF11_DEV_ERR_TIMEOUT;
         }
+        __syncwarp();
     }
     err = __reduce_or_sync(0xFFFFFFFFu, err);
     if (lane == 0) report(P.err, err);
