@@ -976,6 +976,7 @@ struct PrefillShared {
     alignas(1024) uint8_t q[2][kOperand];
     uint8_t k[2][kOperand], v[2][kOperand];
     alignas(16) uint32_t ok[4][4];  // keys of a step that are there; the softmax may read a step's while the next two are decoded
+    float row[2][kPrefillTile];  // factor of a row's scores
     uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], end;
     int32_t sums[kPrefillThreads / 32];
     uint32_t tmem, abort;
@@ -999,11 +1000,15 @@ __device__ __forceinline__ uint64_t swz128_desc(uint32_t low) {
 
 template <class Shared>
 __device__ __forceinline__ bool prefill_wait_slow(uint64_t *bar, uint32_t parity, Shared &S, uint64_t limit_ns) {
-    const uint64_t t0 = global_ns();
-    for (;;) {
+    // the clock is slow to read, and a wait that it delays holds up the others
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait(bar, parity)) return true;
+        if (n % 256) continue;
         if (*reinterpret_cast<volatile uint32_t *>(&S.abort)) return false;
-        if (global_ns() - t0 > limit_ns) {
+        const uint64_t t = global_ns();
+        if (!t0) t0 = t;
+        if (t - t0 > limit_ns) {
             atomicExch(&S.abort, 1u);
             return false;
         }
@@ -1160,39 +1165,49 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
         const int steps = W.a1[x] - W.a0[x];
         float f = 0.0f;
         if (steps) {
-            // the row's queries, scaled by a power of two into FP16's range
-            // (and by the sign of the scores' factor, which is then >= 0)
-            const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(A.q) +
-                                                              token * static_cast<int64_t>(A.q_token_stride) + hq * D);
-            float top = 0.0f;
-            if (live) {
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = __ldg(qp + i);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
-                }
-            }
-            const uint32_t field = __float_as_uint(top) >> 23;
-            const int e = top == 0.0f || field == 255u ? 0 : max(static_cast<int>(field) - 127, -126);
+            // The warp's 32 rows of queries, a row's 16-byte chunks on D / 8 lanes,
+            // all loads in flight at once.  A row is scaled by a power of two
+            // into FP16's range (and by the sign of the scores' factor, which
+            // is then >= 0).
+            constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row; rows at a time
+            const int c = lane % kLanes, base = W.row0 + x * kPrefillTile + (warp & 3) * 32 + lane / kLanes;
             const float f0 = A.scale * P.k_scale * 1.44269504088896341f;
-            float down = e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            if (f0 < 0.0f) down = -down;
-            f = fabsf(f0) * __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-            if (f == 0.0f) f = 1.0f, down = 0.0f;  // all scores 0, and still -inf where masked
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (live) v = __ldg(qp + i);
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint4 v[32 / kAt];
+#pragma unroll
+            for (int i = 0; i < 32 / kAt; ++i) {
+                const int rw = base + i * kAt;
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (rw < W.rows)
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                        static_cast<const uint16_t *>(A.q) +
+                        static_cast<int64_t>(W.q0 + rw / group) * static_cast<int64_t>(A.q_token_stride) +
+                        (head * group + rw % group) * D + c * 8));
+            }
+#pragma unroll
+            for (int i = 0; i < 32 / kAt; ++i) {
+                uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                float top = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    top = max3(top, fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u)));
+#pragma unroll
+                for (int y = 1; y < kLanes; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, y));
+                const uint32_t field = __float_as_uint(top) >> 23;
+                const int e = top == 0.0f || field == 255u ? 0 : max(static_cast<int>(field) - 127, -126);
+                float down = e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                float fr = fabsf(f0) * __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                if (f0 < 0.0f) down = -down;
+                if (fr == 0.0f) fr = 1.0f, down = 0.0f;  // all scores 0, and still -inf where masked
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     w[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
-                *reinterpret_cast<uint4 *>(S.q[x] + (i / 8) * (kPrefillTile * 128) + swz_chunk(r, i % 8)) =
+                const int rt = (warp & 3) * 32 + i * kAt + lane / kLanes;
+                *reinterpret_cast<uint4 *>(S.q[x] + (c / 8) * (kPrefillTile * 128) + swz_chunk(rt, c % 8)) =
                     make_uint4(w[0], w[1], w[2], w[3]);
+                if (c == 0) S.row[x][rt] = fr;
             }
+            __syncwarp();
+            f = S.row[x][r];
             fence_proxy_async_smem();
             mbar_arrive(&S.q_full[x]);
         }
@@ -1235,13 +1250,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
                         if (!(seen >> y & 1u)) s[32 * i + y] = 0xFF800000u;  // -inf
                 }
             }
-            float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[1]);
+            float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[1]), t2 = __uint_as_float(s[2]),
+                  t3 = __uint_as_float(s[3]);
 #pragma unroll
-            for (int i = 2; i < kPrefillTile - 2; i += 4) {
+            for (int i = 4; i < kPrefillTile - 4; i += 8) {
                 t0 = max3(t0, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
                 t1 = max3(t1, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+                t2 = max3(t2, __uint_as_float(s[i + 4]), __uint_as_float(s[i + 5]));
+                t3 = max3(t3, __uint_as_float(s[i + 6]), __uint_as_float(s[i + 7]));
             }
-            const float top = max3(fmaxf(t0, t1), __uint_as_float(s[kPrefillTile - 2]), __uint_as_float(s[kPrefillTile - 1]));
+            t0 = max3(t0, t1, t2);
+            t3 = max3(t3, __uint_as_float(s[kPrefillTile - 4]), __uint_as_float(s[kPrefillTile - 3]));
+            t0 = max3(t0, __uint_as_float(s[kPrefillTile - 2]), __uint_as_float(s[kPrefillTile - 1]));
+            const float top = fmaxf(t0, t3);
             const float mt = top == -INFINITY ? -INFINITY : top * f;
             const bool grow = mt > m + kLazy || (m == -INFINITY && mt != -INFINITY);
             if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -1291,29 +1312,45 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
             tc_fence_after();
         }
         if (!run) err |= DF11_DEV_ERR_TIMEOUT;
+        // Rows out of TMEM into the tile's query operand, which no MMA reads any
+        // more (a thread its own row), and from there to o, a row's chunks on
+        // D / 8 lanes.  l == 0: the row saw no key, whatever the accumulator holds.
+        if (m == -INFINITY) l = 0.0f;
         const float inv = !run ? 0.0f : l > 0.0f ? P.v_scale / l : l;  // NaN stays NaN
-        uint16_t *op = static_cast<uint16_t *>(A.o) + token * static_cast<int64_t>(A.o_token_stride) + hq * D;
+        if (steps) {
 #pragma unroll
-        for (int i = 0; i < D; i += 16) {
-            uint32_t o[16];
-#pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = 0u;
-            if (steps) {
+            for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
                 tc_ld16(o_col + i, o);
                 tc_wait_ld();
-            }
-            if (live) {
 #pragma unroll
                 for (int y = 0; y < 16; y += 8) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        // l == 0: the row saw no key (its accumulator may hold anything finite or not)
-                        const float u = __uint_as_float(o[y + 2 * z]) * inv, v = __uint_as_float(o[y + 2 * z + 1]) * inv;
-                        w[z] = l > 0.0f || l != l ? bf16x2_of(u, v) : 0u;
-                    }
-                    *reinterpret_cast<uint4 *>(op + i + y) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int z = 0; z < 4; ++z)
+                        w[z] = l == 0.0f ? 0u
+                                         : bf16x2_of(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
+                    const int c = (i + y) / 8;
+                    *reinterpret_cast<uint4 *>(S.q[x] + (c / 8) * (kPrefillTile * 128) + swz_chunk(r, c % 8)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
+            }
+            __syncwarp();
+        }
+        {
+            constexpr int kLanes = D / 8, kAt = 32 / kLanes;
+            const int c = lane % kLanes;
+#pragma unroll 4
+            for (int i = 0; i < 32 / kAt; ++i) {
+                const int rt = (warp & 3) * 32 + i * kAt + lane / kLanes, rw = W.row0 + x * kPrefillTile + rt;
+                if (rw >= W.rows) continue;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (steps)
+                    v = *reinterpret_cast<const uint4 *>(S.q[x] + (c / 8) * (kPrefillTile * 128) + swz_chunk(rt, c % 8));
+                *reinterpret_cast<uint4 *>(
+                    static_cast<uint16_t *>(A.o) +
+                    static_cast<int64_t>(W.q0 + rw / group) * static_cast<int64_t>(A.o_token_stride) +
+                    (head * group + rw % group) * D + c * 8) = v;
             }
         }
         if (live && A.lse) A.lse[token * A.n_q_heads + hq] = lse_of(m, l);
