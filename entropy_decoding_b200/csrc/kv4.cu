@@ -12,7 +12,13 @@
 namespace df11 {
 namespace {
 
+// A CTA takes 4 tokens, a thread 16 elements of one of them at a time, of K
+// and of V: one scale, 8 code bytes each, both loads in flight together.
+// Neighbouring threads take the 4 tokens (whose 8-byte pieces of V codes and
+// bytes of V scales are neighbours where the tokens are), then the blocks of a
+// row, which are contiguous in the rows and, within a head, in the K codes.
 constexpr int kKv4Threads = 256;
+constexpr int kKv4Tokens = 4;
 
 struct Kv4Params {
     uint8_t *pages;
@@ -27,28 +33,6 @@ struct Kv4Params {
     uint64_t k_stride, v_stride;
     void *k_out, *v_out;  // gather
 };
-
-// A thread handles 16 elements of one head of one token, of K (blockIdx.y 0)
-// or V (1): one scale, 8 code bytes.  `u` numbers them so that neighbouring
-// threads touch neighbouring bytes of the cache: K by block within the token
-// (a head's row is contiguous), V by token within 4 (their 8-byte pieces are).
-template <int D>
-__device__ __forceinline__ void unit(const Kv4Params &P, bool is_v, uint64_t u, uint32_t &t, uint32_t &h, uint32_t &b) {
-    constexpr uint32_t NB = D / kKv4Group;
-    if (is_v) {
-        const uint32_t c = static_cast<uint32_t>(u & 3u);
-        const uint64_t w = u >> 2;
-        b = static_cast<uint32_t>(w % NB);
-        const uint64_t x = w / NB;
-        h = static_cast<uint32_t>(x % P.n_heads);
-        t = static_cast<uint32_t>(x / P.n_heads) * 4u + c;
-    } else {
-        b = static_cast<uint32_t>(u % NB);
-        const uint64_t x = u / NB;
-        h = static_cast<uint32_t>(x % P.n_heads);
-        t = static_cast<uint32_t>(x / P.n_heads);
-    }
-}
 
 // Places of the codes and the scale of block b of head h in slot `slot`.
 template <int D>
@@ -66,9 +50,10 @@ __device__ __forceinline__ void place(const Kv4Params &P, bool is_v, uint64_t sl
     }
 }
 
-// Slot of token t: false for a negative one, and (flagged) past the cache.
-__device__ __forceinline__ bool slot_of(const Kv4Params &P, uint32_t t, uint64_t &slot) {
-    const int64_t s = P.slots[t];
+// Slot of token t: false past the tokens, for a negative one, and (flagged) past the cache.
+__device__ __forceinline__ bool slot_of(const Kv4Params &P, int64_t t, uint64_t &slot) {
+    if (t >= P.n_tokens) return false;
+    const int64_t s = __ldg(P.slots + t);
     if (s < 0) return false;
     slot = static_cast<uint64_t>(s);
     if (slot < P.n_slots) return true;
@@ -76,110 +61,175 @@ __device__ __forceinline__ bool slot_of(const Kv4Params &P, uint32_t t, uint64_t
     return false;
 }
 
-// The scale and the codes follow the definition step by step with IEEE
-// division: a block's scale has 4 significant bits and an element 8, so
-// quotients fall exactly on the borders between levels often, and a
-// reciprocal's last bit would move them.
-template <bool FP32, int D>
-__global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Params P) {
-    const bool is_v = blockIdx.y;
-    uint32_t t, h, b;
-    unit<D>(P, is_v, static_cast<uint64_t>(blockIdx.x) * kKv4Threads + threadIdx.x, t, h, b);
-    uint64_t slot;
-    if (t >= static_cast<uint32_t>(P.n_tokens) || !slot_of(P, t, slot)) return;
-    const uint64_t at = t * (is_v ? P.v_stride : P.k_stride) + h * D + b * kKv4Group;
-    const void *src = is_v ? P.v : P.k;
-    float x[2][8];
-    if constexpr (FP32) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = __ldg(p + i);
-            const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[i / 2][4 * (i % 2) + j] = __bfloat162float(__float2bfloat16_rn(f[j]));
-        }
+// 32 bytes, a whole sector, in one instruction where the address allows it
+// (rows need only be 16-byte aligned; the branch is the same for all threads).
+__device__ __forceinline__ void load32(const void *p, uint32_t *w) {
+    if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
     } else {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + at);
+        const uint4 a = __ldg(static_cast<const uint4 *>(p)), b = __ldg(static_cast<const uint4 *>(p) + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
+    if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Sixteen elements as they lie in memory.
+template <bool FP32>
+struct Sixteen {
+    uint32_t w[FP32 ? 16 : 8];
+    __device__ __forceinline__ void load(const void *p, uint64_t i) {
+        const uint8_t *q = static_cast<const uint8_t *>(p) + i * (FP32 ? 4 : 2);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 v = __ldg(p + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int j = 0; j < (FP32 ? 2 : 1); ++j) load32(q + 32 * j, w + 8 * j);
+    }
+    // as BF16 values
+    __device__ __forceinline__ void get(float (&x)[16]) const {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[i][2 * j] = __uint_as_float(w[j] << 16);
-                x[i][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int i = 0; i < (FP32 ? 16 : 8); ++i) {
+            if constexpr (FP32) {
+                x[i] = __bfloat162float(__float2bfloat16_rn(__uint_as_float(w[i])));
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
             }
         }
     }
+};
+
+// x / d correctly rounded, from r = 1 / d correctly rounded, by one residual
+// step (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", theorem on division with a correct reciprocal), for
+// |x / d| <= 8 and d well inside the exponent range.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, d, x), r, q);
+}
+
+// The scale and the codes follow the definition step by step with correctly
+// rounded quotients: a block's scale has 4 significant bits and an element 8,
+// so quotients fall exactly on the borders between levels often, and a
+// reciprocal's last bit would move them.  A division per element took 34 us
+// for 16,384 tokens of 8 heads of 128; read and write are bound by memory so.
+__device__ __forceinline__ void quantize(const float (&x)[16], float g, uint2 &codes, uint32_t &scale) {
     float top = 0.0f;  // fmaxf leaves NaN out
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i / 8][i % 8]));
-    const float g = is_v ? P.v_scale : P.k_scale;
-    const uint32_t sb = f32_to_e4m3(fminf(__fdiv_rn(__fdiv_rn(top, 6.0f), g), 448.0f));
-    const uint32_t sh = e4m3x2_to_f16x2(sb);
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+    scale = f32_to_e4m3(fminf(__fdiv_rn(__fdiv_rn(top, 6.0f), g), 448.0f));
+    const uint32_t sh = e4m3x2_to_f16x2(scale);
     float s;
-    asm("cvt.f32.f16 %0, %1;" : "=f"(s) : "h"(static_cast<uint16_t>(sh)));
+    asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(s) : "r"(sh));
     const float step = s * g;
-    uint2 codes = make_uint2(0u, 0u);
-    if (step > 0.0f) {
+    codes = make_uint2(0u, 0u);
+    if (!(step > 0.0f)) return;
+    float y[2][8];
+    if (step > 0x1p-100f && step < 0x1p100f) {
+        // what saturates anyway is brought to 8 steps first; a NaN goes with the positive ones
+        const float r = __frcp_rn(step), most = 8.0f * step;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i / 8][i % 8] = __fdiv_rn(x[i / 8][i % 8], step);
-        codes = make_uint2(f32x8_to_e2m1(x[0]), f32x8_to_e2m1(x[1]));
+        for (int i = 0; i < 16; ++i) y[i / 8][i % 8] = quotient(fmaxf(fminf(x[i], most), -most), step, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i / 8][i % 8] = __fdiv_rn(x[i], step);
     }
-    uint8_t *cp, *sp;
-    place<D>(P, is_v, slot, h, b, &cp, &sp);
-    *reinterpret_cast<uint2 *>(cp) = codes;
-    *sp = static_cast<uint8_t>(sb);
+    codes = make_uint2(f32x8_to_e2m1(y[0]), f32x8_to_e2m1(y[1]));
+}
+
+template <bool FP32, int D>
+__global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Params P) {
+    constexpr uint32_t NB = D / kKv4Group;
+    const uint32_t units = kKv4Tokens * NB * P.n_heads;
+    for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
+        const int64_t t = static_cast<int64_t>(blockIdx.x) * kKv4Tokens + u % kKv4Tokens;
+        const uint32_t hb = u / kKv4Tokens;  // block of the row
+        uint64_t slot;
+        if (!slot_of(P, t, slot)) continue;
+        Sixteen<FP32> rk, rv;
+        rk.load(P.k, t * P.k_stride + hb * kKv4Group);
+        rv.load(P.v, t * P.v_stride + hb * kKv4Group);
+#pragma unroll
+        for (int is_v = 0; is_v < 2; ++is_v) {
+            float x[16];
+            (is_v ? rv : rk).get(x);
+            uint2 codes;
+            uint32_t scale;
+            quantize(x, is_v ? P.v_scale : P.k_scale, codes, scale);
+            uint8_t *cp, *sp;
+            place<D>(P, is_v, slot, hb / NB, hb % NB, &cp, &sp);
+            *reinterpret_cast<uint2 *>(cp) = codes;
+            *sp = static_cast<uint8_t>(scale);
+        }
+    }
 }
 
 // level * s is exact in FP16 (2 and 4 significant bits, at most 6 * 448); the
 // product with the cache's scale is rounded to FP32 and then to the output.
 template <bool FP32, int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_gather_kernel(const Kv4Params P) {
-    const bool is_v = blockIdx.y;
-    uint32_t t, h, b;
-    unit<D>(P, is_v, static_cast<uint64_t>(blockIdx.x) * kKv4Threads + threadIdx.x, t, h, b);
-    void *dst = is_v ? P.v_out : P.k_out;
-    uint64_t slot;
-    if (!dst || t >= static_cast<uint32_t>(P.n_tokens) || !slot_of(P, t, slot)) return;
-    uint8_t *cp, *sp;
-    place<D>(P, is_v, slot, h, b, &cp, &sp);
-    const uint2 codes = *reinterpret_cast<const uint2 *>(cp);
-    const uint32_t s2 = e4m3x2_to_f16x2(*sp * 0x0101u);
-    const float g = is_v ? P.v_scale : P.k_scale;
-    float y[16];
+    constexpr uint32_t NB = D / kKv4Group;
+    const uint32_t units = kKv4Tokens * NB * P.n_heads;
+    for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
+        const int64_t t = static_cast<int64_t>(blockIdx.x) * kKv4Tokens + u % kKv4Tokens;
+        const uint32_t hb = u / kKv4Tokens;
+        uint64_t slot;
+        if (!slot_of(P, t, slot)) continue;
+        uint2 codes[2];
+        uint32_t scale[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t r[4];
-        e2m1x8_to_f16(i ? codes.y : codes.x, r);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t v = f16x2_mul(r[j], s2);
-            float lo, hi;
-            asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                : "=f"(lo), "=f"(hi)
-                : "r"(v));
-            y[8 * i + 2 * j] = lo * g;
-            y[8 * i + 2 * j + 1] = hi * g;
+        for (int is_v = 0; is_v < 2; ++is_v) {
+            if (!(is_v ? P.v_out : P.k_out)) continue;
+            uint8_t *cp, *sp;
+            place<D>(P, is_v, slot, hb / NB, hb % NB, &cp, &sp);
+            codes[is_v] = *reinterpret_cast<const uint2 *>(cp);
+            scale[is_v] = *sp;
         }
-    }
-    const uint64_t at = (static_cast<uint64_t>(t) * P.n_heads + h) * D + b * kKv4Group;
-    if constexpr (FP32) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(dst) + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-    } else {
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + at);
+        for (int is_v = 0; is_v < 2; ++is_v) {
+            void *dst = is_v ? P.v_out : P.k_out;
+            if (!dst) continue;
+            const uint32_t s2 = e4m3x2_to_f16x2(scale[is_v] * 0x0101u);
+            const float g = is_v ? P.v_scale : P.k_scale;
+            float y[16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t w[4];
+            for (int i = 0; i < 2; ++i) {
+                uint32_t r[4];
+                e2m1x8_to_f16(i ? codes[is_v].y : codes[is_v].x, r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(y[8 * i + 2 * j], y[8 * i + 2 * j + 1]);
-                w[j] = *reinterpret_cast<const uint32_t *>(&p);
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t v = f16x2_mul(r[j], s2);
+                    float lo, hi;
+                    asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+                        : "=f"(lo), "=f"(hi)
+                        : "r"(v));
+                    y[8 * i + 2 * j] = lo * g;
+                    y[8 * i + 2 * j + 1] = hi * g;
+                }
             }
-            o[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            const uint64_t at = (static_cast<uint64_t>(t) * P.n_heads * NB + hb) * kKv4Group;
+            uint32_t w[FP32 ? 16 : 8];
+#pragma unroll
+            for (int i = 0; i < (FP32 ? 16 : 8); ++i) {
+                if constexpr (FP32) {
+                    w[i] = __float_as_uint(y[i]);
+                } else {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&p);
+                }
+            }
+            uint8_t *o = static_cast<uint8_t *>(dst) + at * (FP32 ? 4 : 2);
+#pragma unroll
+            for (int i = 0; i < (FP32 ? 2 : 1); ++i) store32(o + 32 * i, w + 8 * i);
         }
     }
 }
@@ -199,10 +249,12 @@ Kv4Params params(const df11_kv4_cache &c, const int64_t *slots, int n_tokens, in
     return P;
 }
 
-// units of K or V, the tokens rounded up to whole groups of 4
-dim3 grid_of(const df11_kv4_cache &c, int n_tokens) {
-    const uint64_t units = (static_cast<uint64_t>(n_tokens) + 3) / 4 * 4 * c.n_heads * (c.head_dim / kKv4Group);
-    return dim3(static_cast<unsigned>((units + kKv4Threads - 1) / kKv4Threads), 2);
+unsigned ctas_of(int n_tokens) { return static_cast<unsigned>((static_cast<int64_t>(n_tokens) + kKv4Tokens - 1) / kKv4Tokens); }
+
+// A thread per unit of the CTA's tokens, in whole warps, as far as they go.
+unsigned threads_of(const df11_kv4_cache &c) {
+    const unsigned units = kKv4Tokens * static_cast<unsigned>(c.n_heads) * (c.head_dim / kKv4Group);
+    return units < kKv4Threads ? (units + 31) / 32 * 32 : kKv4Threads;
 }
 
 }  // namespace
@@ -215,13 +267,13 @@ LaunchStatus launch_kv4_append(const df11_kv4_cache &c, const void *k, uint64_t 
     P.v = v;
     P.k_stride = k_stride;
     P.v_stride = v_stride;
-    const dim3 grid = grid_of(c, n_tokens);
+    const unsigned grid = ctas_of(n_tokens), threads = threads_of(c);
     if (c.head_dim == 128)
-        fp32 ? kv4_append_kernel<true, 128><<<grid, kKv4Threads, 0, s>>>(P)
-             : kv4_append_kernel<false, 128><<<grid, kKv4Threads, 0, s>>>(P);
+        fp32 ? kv4_append_kernel<true, 128><<<grid, threads, 0, s>>>(P)
+             : kv4_append_kernel<false, 128><<<grid, threads, 0, s>>>(P);
     else
-        fp32 ? kv4_append_kernel<true, 64><<<grid, kKv4Threads, 0, s>>>(P)
-             : kv4_append_kernel<false, 64><<<grid, kKv4Threads, 0, s>>>(P);
+        fp32 ? kv4_append_kernel<true, 64><<<grid, threads, 0, s>>>(P)
+             : kv4_append_kernel<false, 64><<<grid, threads, 0, s>>>(P);
     return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;
 }
 
@@ -230,13 +282,13 @@ LaunchStatus launch_kv4_gather(const df11_kv4_cache &c, const int64_t *slots, in
     Kv4Params P = params(c, slots, n_tokens, err);
     P.k_out = k_out;
     P.v_out = v_out;
-    const dim3 grid = grid_of(c, n_tokens);
+    const unsigned grid = ctas_of(n_tokens), threads = threads_of(c);
     if (c.head_dim == 128)
-        fp32 ? kv4_gather_kernel<true, 128><<<grid, kKv4Threads, 0, s>>>(P)
-             : kv4_gather_kernel<false, 128><<<grid, kKv4Threads, 0, s>>>(P);
+        fp32 ? kv4_gather_kernel<true, 128><<<grid, threads, 0, s>>>(P)
+             : kv4_gather_kernel<false, 128><<<grid, threads, 0, s>>>(P);
     else
-        fp32 ? kv4_gather_kernel<true, 64><<<grid, kKv4Threads, 0, s>>>(P)
-             : kv4_gather_kernel<false, 64><<<grid, kKv4Threads, 0, s>>>(P);
+        fp32 ? kv4_gather_kernel<true, 64><<<grid, threads, 0, s>>>(P)
+             : kv4_gather_kernel<false, 64><<<grid, threads, 0, s>>>(P);
     return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;
 }
 

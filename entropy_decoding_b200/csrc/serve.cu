@@ -130,24 +130,35 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const df11_kv
 
 // ------------------------------------------------------------------ norm and rotation
 
-// head_dim / 8 lanes hold a head, 8 elements (4 pairs) each; a thread keeps
-// its 4 pairs' sines and cosines of one token and walks over that token's
-// heads, so the 64-bit angle and the sincos are paid once per token.  The
-// pass reads each element once and writes it once; nothing else goes to
-// memory.
-constexpr int kRopeThreads = 256;
+// A CTA takes a token, head_dim / 8 lanes a head, 8 elements (4 pairs) each.
+// The 64-bit angle and the sincos of a pair are paid once per token, while the
+// heads' loads are on their way.  The pass reads each element once and writes
+// it once; nothing else goes to memory.
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBatch = 5;  // heads whose loads a thread has in flight
 
+// Four elements as they lie in memory, and as floats.
 template <bool FP32>
-__device__ __forceinline__ void load4(const void *p, int64_t i, float *v) {
-    if constexpr (FP32) {
-        const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    } else {
-        const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+struct Four;
+template <>
+struct Four<true> {
+    float4 a;
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    }
+    __device__ __forceinline__ void get(float *v) const { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
+};
+template <>
+struct Four<false> {
+    uint2 a;
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        a = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    }
+    __device__ __forceinline__ void get(float *v) const {
         v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xFFFF0000u);
         v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xFFFF0000u);
     }
-}
+};
 
 __device__ __forceinline__ void store4(void *p, int64_t i, const float *v) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
@@ -169,64 +180,89 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const df11_q
     const bool rotated = 4 * j < half;
     const bool split = rotated && !INTER;
     const int oa = split ? 4 * j : 8 * j, ob = split ? 4 * j + half : 8 * j + 4;
-    float cs[4], sn[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = 1.0f, sn[i] = 0.0f;
-    if (rotated) {
-        const double pos = A.positions[t];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // in half turns, reduced to [-1, 1] in 64 bits: what 32 bits then
-            // round is the remainder, however far the position
-            double x = pos * A.inv_freq[4 * j + i] * 0.31830988618379067154;
-            x -= 2.0 * rint(0.5 * x);
-            sincospif(static_cast<float>(x), &sn[i], &cs[i]);
-        }
-    }
-    float w[2][8];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const void *wp = s ? A.k.weight : A.q.weight;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[s][i] = 1.0f;
-        if (wp) {
-            load4<false>(wp, oa, w[s]);
-            load4<false>(wp, ob, w[s] + 4);
-        }
-    }
     const uint32_t group = (L == 32 ? 0xFFFFFFFFu : (1u << (L % 32)) - 1u) << (threadIdx.x & 31 & ~(L - 1));
     const int heads = A.q.n_heads + A.k.n_heads;
-    for (int h = blockIdx.y * kHeads + threadIdx.x / L; h < heads; h += gridDim.y * kHeads) {
+    const int h0 = blockIdx.y * kHeads + threadIdx.x / L, dh = gridDim.y * kHeads;
+    // a batch of heads at a time, its loads in flight together, the first
+    // batch's while the angles are made
+    Four<FP32> xa[kRopeBatch], xb[kRopeBatch];
+    auto side = [&](int h, int64_t &hd) -> const df11_rope_side & {
         const bool is_k = h >= A.q.n_heads;
-        const df11_rope_side &S = is_k ? A.k : A.q;
-        const int64_t hd = static_cast<int64_t>(is_k ? h - A.q.n_heads : h) * D;
-        float v[8];
-        const int64_t at = t * static_cast<int64_t>(S.token_stride) + hd;
-        load4<FP32>(S.x, at + oa, v);
-        load4<FP32>(S.x, at + ob, v + 4);
-        if (S.weight) {
-            float ss = 0.0f;
+        hd = static_cast<int64_t>(is_k ? h - A.q.n_heads : h) * D;
+        return is_k ? A.k : A.q;
+    };
+    auto fetch = [&](int hb) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1)
-                ss += __shfl_xor_sync(group, ss, o);
-            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + A.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * (is_k ? w[1][i] : w[0][i]);
+        for (int b = 0; b < kRopeBatch; ++b) {
+            const int h = hb + b * dh;
+            if (h >= heads) break;
+            int64_t hd;
+            const df11_rope_side &S = side(h, hd);
+            const int64_t at = t * static_cast<int64_t>(S.token_stride) + hd;
+            xa[b].load(S.x, at + oa);
+            xb[b].load(S.x, at + ob);
         }
-        if (rotated) {
+    };
+    fetch(h0);
+    // a thread per pair; the heads' threads read them from shared memory
+    __shared__ __align__(16) float s_cos[D / 2], s_sin[D / 2];
+    for (int p = threadIdx.x; p < half; p += kRopeThreads) {
+        // in half turns, reduced to [-1, 1] in 64 bits: what 32 bits then
+        // round is the remainder, however far the position
+        double x = A.positions[t] * A.inv_freq[p] * 0.31830988618379067154;
+        x -= 2.0 * rint(0.5 * x);
+        sincospif(static_cast<float>(x), &s_sin[p], &s_cos[p]);
+    }
+    Four<false> wq[2] = {}, wk[2] = {};
+    if (A.q.weight) wq[0].load(A.q.weight, oa), wq[1].load(A.q.weight, ob);
+    if (A.k.weight) wk[0].load(A.k.weight, oa), wk[1].load(A.k.weight, ob);
+    __syncthreads();
+    float cs[4] = {}, sn[4] = {};
+    if (rotated) {
+        Four<true> c, s;
+        c.load(s_cos, 4 * j);
+        s.load(s_sin, 4 * j);
+        c.get(cs);
+        s.get(sn);
+    }
+    for (int hb = h0; hb < heads; hb += kRopeBatch * dh) {
+        if (hb != h0) fetch(hb);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float &a = v[INTER ? 2 * i : i], &b = v[INTER ? 2 * i + 1 : i + 4];
-                const float ra = a * cs[i] - b * sn[i];
-                b = b * cs[i] + a * sn[i];
-                a = ra;
+        for (int b = 0; b < kRopeBatch; ++b) {
+            const int h = hb + b * dh;
+            if (h >= heads) break;
+            const bool is_k = h >= A.q.n_heads;
+            int64_t hd;
+            const df11_rope_side &S = side(h, hd);
+            float v[8];
+            xa[b].get(v);
+            xb[b].get(v + 4);
+            if (S.weight) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
+#pragma unroll
+                for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+                const float inv = 1.0f / sqrtf(ss * (1.0f / D) + A.eps);
+                float w[8];
+                (is_k ? wk[0] : wq[0]).get(w);
+                (is_k ? wk[1] : wq[1]).get(w + 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
             }
+            if (rotated) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float &a = v[INTER ? 2 * i : i], &c = v[INTER ? 2 * i + 1 : i + 4];
+                    const float ra = a * cs[i] - c * sn[i];
+                    c = c * cs[i] + a * sn[i];
+                    a = ra;
+                }
+            }
+            const int64_t to = t * static_cast<int64_t>(S.out_token_stride) + hd;
+            store4(S.out, to + oa, v);
+            store4(S.out, to + ob, v + 4);
         }
-        const int64_t to = t * static_cast<int64_t>(S.out_token_stride) + hd;
-        store4(S.out, to + oa, v);
-        store4(S.out, to + ob, v + 4);
     }
 }
 
