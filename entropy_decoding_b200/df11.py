@@ -531,32 +531,34 @@ def df11_decode_gemm_launch_shape(mats, m: int):
 
 
 # ----------------------------------------------------------------- serving a block
+#
+# These run once per layer and token: pointers go to the library as they are (0 and None are NULL), with as little
+# Python in between as it takes.
+
+_kv_extend, _qk_norm_rope = _lib.df11_kv_extend, _lib.df11_qk_norm_rope
+_kv4_append, _kv4_gather, _kv4_attention = _lib.df11_kv4_append, _lib.df11_kv4_gather, _lib.df11_kv4_attention
+
 
 def df11_kv_extend(kv_lens_ptr: int, new_lens_ptr: int, n_reqs: int, free_pages_ptr: int, n_free_ptr: int,
                    block_table_ptr: int, max_pages: int, page_size: int, kv_lens_out_ptr: int, q_start_ptr: int,
                    slots_ptr: int, positions_ptr: int, max_tokens: int, n_free_out_ptr: int,
                    err_ptr: int | None = None, stream: int = 0):
     """One step's pages, block tables, slots and positions from the requests' lengths, all on the device."""
-    a = KvExtendArgs(kv_lens_ptr or None, new_lens_ptr or None, n_reqs, max_pages, free_pages_ptr or None,
-                     n_free_ptr or None, block_table_ptr or None, page_size, max_tokens, kv_lens_out_ptr or None,
-                     q_start_ptr or None, slots_ptr or None, positions_ptr or None, n_free_out_ptr or None)
-    _check(_lib.df11_kv_extend(a, err_ptr or None, stream or None), "df11_kv_extend")
-
-
-def _rope_side(side) -> RopeSide:
-    if side is None:
-        return RopeSide()
-    x, stride, weight, out, out_stride, n_heads = side
-    return RopeSide(x or None, stride, weight or None, out or None, out_stride, n_heads)
+    st = _kv_extend(KvExtendArgs(kv_lens_ptr, new_lens_ptr, n_reqs, max_pages, free_pages_ptr, n_free_ptr,
+                                 block_table_ptr, page_size, max_tokens, kv_lens_out_ptr, q_start_ptr, slots_ptr,
+                                 positions_ptr, n_free_out_ptr), err_ptr, stream)
+    if st:
+        raise Df11Error(st, "df11_kv_extend")
 
 
 def df11_qk_norm_rope(q, k, n_tokens: int, head_dim: int, positions_ptr: int, inv_freq_ptr: int, rot_dim: int,
                       interleaved: bool = False, eps: float = 1e-6, dtype: str = "fp32", stream: int = 0):
     """q, k: (x pointer, token stride, norm weight pointer or 0, out pointer, out token stride, heads), strides in
     elements, or None: that side is absent.  dtype: of x, "fp32" or "bf16"; out is BF16."""
-    a = QkNormRopeArgs(_rope_side(q), _rope_side(k), n_tokens, head_dim, rot_dim, int(interleaved), ACTIVATIONS[dtype],
-                       eps, positions_ptr or None, inv_freq_ptr or None)
-    _check(_lib.df11_qk_norm_rope(a, stream or None), "df11_qk_norm_rope")
+    st = _qk_norm_rope(QkNormRopeArgs(q or (), k or (), n_tokens, head_dim, rot_dim, interleaved, ACTIVATIONS[dtype], eps,
+                                      positions_ptr, inv_freq_ptr), stream)
+    if st:
+        raise Df11Error(st, "df11_qk_norm_rope")
 
 
 def df11_kv4_page_bytes(page_size: int, n_heads: int, head_dim: int) -> int:
@@ -566,14 +568,17 @@ def df11_kv4_page_bytes(page_size: int, n_heads: int, head_dim: int) -> int:
 
 def df11_kv4_append(cache: Kv4Cache, k_ptr: int, k_token_stride: int, v_ptr: int, v_token_stride: int, slots_ptr: int,
                     n_tokens: int, dtype: str = "bf16", err_ptr: int | None = None, stream: int = 0):
-    _check(_lib.df11_kv4_append(cache, k_ptr or None, k_token_stride, v_ptr or None, v_token_stride, slots_ptr or None,
-                                n_tokens, ACTIVATIONS[dtype], err_ptr or None, stream or None), "df11_kv4_append")
+    st = _kv4_append(cache, k_ptr, k_token_stride, v_ptr, v_token_stride, slots_ptr, n_tokens, ACTIVATIONS[dtype], err_ptr,
+                     stream)
+    if st:
+        raise Df11Error(st, "df11_kv4_append")
 
 
 def df11_kv4_gather(cache: Kv4Cache, slots_ptr: int, n_tokens: int, k_out_ptr: int, v_out_ptr: int,
                     dtype: str = "bf16", err_ptr: int | None = None, stream: int = 0):
-    _check(_lib.df11_kv4_gather(cache, slots_ptr or None, n_tokens, k_out_ptr or None, v_out_ptr or None,
-                                ACTIVATIONS[dtype], err_ptr or None, stream or None), "df11_kv4_gather")
+    st = _kv4_gather(cache, slots_ptr, n_tokens, k_out_ptr, v_out_ptr, ACTIVATIONS[dtype], err_ptr, stream)
+    if st:
+        raise Df11Error(st, "df11_kv4_gather")
 
 
 def df11_kv4_attention_workspace_bytes(cache: Kv4Cache, n_q_heads: int, n_reqs: int, n_tokens: int,
@@ -588,10 +593,12 @@ def df11_kv4_attention(cache: Kv4Cache, q_ptr: int, q_token_stride: int, o_ptr: 
                        max_pages: int, n_tokens: int, max_q_len: int, scale: float, workspace_ptr: int,
                        workspace_bytes: int, causal: bool = True, window: int = 0, lse_ptr: int | None = None,
                        err_ptr: int | None = None, stream: int = 0):
-    a = Kv4AttentionArgs(q_ptr or None, q_token_stride, o_ptr or None, o_token_stride, lse_ptr or None,
-                         q_start_ptr or None, kv_lens_ptr or None, block_table_ptr or None, n_reqs, max_pages, n_tokens,
-                         n_q_heads, max_q_len, int(causal), window, scale, workspace_ptr or None, workspace_bytes)
-    _check(_lib.df11_kv4_attention(cache, a, err_ptr or None, stream or None), "df11_kv4_attention")
+    st = _kv4_attention(cache, Kv4AttentionArgs(q_ptr, q_token_stride, o_ptr, o_token_stride, lse_ptr, q_start_ptr,
+                                                kv_lens_ptr, block_table_ptr, n_reqs, max_pages, n_tokens, n_q_heads,
+                                                max_q_len, causal, window, scale, workspace_ptr, workspace_bytes),
+                        err_ptr, stream)
+    if st:
+        raise Df11Error(st, "df11_kv4_attention")
 
 
 # ----------------------------------------------------------------- torch-side helpers (device memory only)
