@@ -47,6 +47,12 @@ constexpr int kSplitKeys = 64;     // keys of a chunk: a warp's step
 constexpr int kSplitStages = 2;    // chunks that a warp has room for
 constexpr int kSplitMaxRows = 64;  // rows (tokens x heads of a group) of a request that go this way
 constexpr int kSplitAlign = 4 * kSplitWarps;  // units of at most so many chunks are not shared between CTAs
+// What a unit costs a CTA beside its chunks (queries, joins), in chunks: shares
+// are equal in this measure, in which a unit starts with so many empty places.
+// 64 requests of 256 to 16384 keys (8 cache heads of 128, groups of 4) take 182 us
+// with 0, 167 with 6, 160 with 10, 155 with 16 and 156 with 20; 2 of 98301 to
+// 131072 keys 67, 67, 65, 65 and 64.
+constexpr int kSplitUnitCost = 16;
 constexpr int32_t kMaxKeys = INT32_MAX - 255;
 
 // A partial result in the workspace: unnormalised O (8 x D), then m and l.
@@ -525,16 +531,59 @@ __device__ __forceinline__ void split_store(const AttnParams &P, const SplitPos 
     if (A.lse && d == 0) A.lse[token * A.n_q_heads + hq] = lse_of(m, l);
 }
 
-// CTA b's share of the launch's chunks starts here: equal parts, the first total % ctas one longer.
+// CTA b's share of the launch's places starts here: equal parts, the first total % ctas one longer.
 struct SplitShares {
     int base, rem;
     __device__ __forceinline__ int start(int b) const { return b * base + min(b, rem); }
-    // The CTA that has chunk y.
+    // The CTA that has place y.
     __device__ __forceinline__ int owner(int y) const {
         const int longer = rem * (base + 1);
         return y < longer ? y / (base + 1) : rem + (y - longer) / base;
     }
 };
+
+// A place in the launch: its request, the unit there, the offset in it, and the
+// places and the chunks before it.
+struct SplitPlace {
+    int r, unit, off, chunks;  // chunks: of each of the request's units
+    int at, before;            // the place itself; chunks of units before it, and its own unit's before it
+};
+
+// Both ends of a share at once, by all lanes of a warp.
+__device__ __forceinline__ void split_find(const AttnParams &P, int lane, SplitPlace (&p)[2]) {
+    int base = 0, units = 0;
+    for (int b = 0; b < P.a.n_reqs && base <= p[1].at; b += 32) {
+        SplitReq q{};
+        if (b + lane < P.a.n_reqs) q = split_req(P, b + lane);
+        const int w = q.units * (q.chunks + kSplitUnitCost);
+        int incl = w, uncl = q.units;
+#pragma unroll
+        for (int y = 1; y < 32; y <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, incl, y), v = __shfl_up_sync(0xFFFFFFFFu, uncl, y);
+            if (lane >= y) incl += o, uncl += v;
+        }
+        const int at = base + incl - w, before = units + uncl - q.units;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t holds = __ballot_sync(0xFFFFFFFFu, w && at <= p[i].at && p[i].at < at + w);
+            if (!holds) continue;
+            const int src = __ffs(holds) - 1, size = q.chunks + kSplitUnitCost, in = p[i].at - at;
+            const int unit = size > 0 ? in / size : 0;
+            p[i].r = b + src;
+            p[i].unit = __shfl_sync(0xFFFFFFFFu, unit, src);
+            p[i].off = __shfl_sync(0xFFFFFFFFu, in - unit * size, src);
+            p[i].chunks = __shfl_sync(0xFFFFFFFFu, q.chunks, src);
+            // empty places before it: those of the units before, and its own unit's
+            p[i].before = p[i].at - (__shfl_sync(0xFFFFFFFFu, before + unit, src)) * kSplitUnitCost - min(p[i].off, kSplitUnitCost);
+        }
+        base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        units += __shfl_sync(0xFFFFFFFFu, uncl, 31);
+    }
+    if (base <= p[1].at) {  // the end of the launch
+        p[1].off = 0;
+        p[1].before = base - units * kSplitUnitCost;
+    }
+}
 
 // Waits until every lane's flag word (null: none), but for the bits `loose`,
 // holds `want`; false after limit_ns, which sets *dead, or when *dead is set.
@@ -606,7 +655,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     int total = 0, longest = 0;
     for (int r = lane; r < A.n_reqs; r += 32) {
         const SplitReq q = split_req(P, r);
-        total += q.units * q.chunks;
+        total += q.units * (q.chunks + kSplitUnitCost);
         if (q.units) longest = max(longest, q.chunks);
         if (blockIdx.x == 0 && warp == 0) {
             if (!rows_valid(A, __ldg(A.q_start + r), __ldg(A.q_start + r + 1))) err |= DF11_DEV_ERR_AUX;
@@ -616,60 +665,38 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     total = static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(total)));
     const bool aligned = __reduce_max_sync(0xFFFFFFFFu, longest) <= kSplitAlign;
     __syncthreads();
-    // no share is empty: a unit's parts are then those of every CTA from its first to its last
     const int ctas = min(static_cast<int>(gridDim.x), total);
     if (static_cast<int>(blockIdx.x) >= ctas) {
         report(P.err, err);
         return;
     }
+    // ---- the share: no share of places is empty, and a unit's chunks follow one
+    // another, so its parts are those of every CTA from its first chunk's to its last's
     const SplitShares shares{total / ctas, total % ctas};
-    int x0 = shares.start(blockIdx.x), x1 = shares.start(blockIdx.x + 1);
-    // ---- the share's start as a position; an aligned share's ends moved to the next unit starts
-    SplitPos ahead;  // of this warp's next chunk to copy
-    {
-        int base = 0, off = 0, end = x1, req = 0;
-        for (int b = 0; b < A.n_reqs && base <= x1; b += 32) {
-            SplitReq q{};
-            if (b + lane < A.n_reqs) q = split_req(P, b + lane);
-            const int w = q.units * q.chunks;
-            int incl = w;
+    SplitPlace ends[2];
+    ends[0].at = shares.start(blockIdx.x);
+    ends[1].at = shares.start(blockIdx.x + 1);
+    split_find(P, lane, ends);
+    // first places of the units that the ends lie in
+    const int unit0 = ends[0].at - ends[0].off, unit1 = ends[1].at - ends[1].off;
+    if (aligned) {
+        // both ends move to the next unit's start
 #pragma unroll
-            for (int y = 1; y < 32; y <<= 1) {
-                const int o = __shfl_up_sync(0xFFFFFFFFu, incl, y);
-                if (lane >= y) incl += o;
-            }
-            const int at = base + incl - w;
-            const uint32_t holds0 = __ballot_sync(0xFFFFFFFFu, w && at <= x0 && x0 < at + w);
-            const uint32_t holds1 = __ballot_sync(0xFFFFFFFFu, w && at < x1 && x1 < at + w);
-            if (holds0) {
-                const int src = __ffs(holds0) - 1;
-                req = b + src;
-                off = __shfl_sync(0xFFFFFFFFu, x0 - at, src);
-            }
-            if (holds1 && aligned) {
-                const int chunks = max(q.chunks, 1);
-                end = __shfl_sync(0xFFFFFFFFu, at + (x1 - at + chunks - 1) / chunks * chunks, __ffs(holds1) - 1);
-            }
-            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
-        }
-        ahead.r = req;
-        ahead.q = split_req(P, req);
-        const int unit = off / ahead.q.chunks;
-        ahead.head = unit / ahead.q.tiles;
-        ahead.tile = unit % ahead.q.tiles;
-        ahead.c = off - unit * ahead.q.chunks;
-        x1 = end;
-        if (aligned && ahead.c) {
-            const int skip = ahead.q.chunks - ahead.c;
-            x0 += skip;
-            if (x0 < x1) ahead.advance(P, skip);
-        }
-        if (x0 >= x1) {
-            report(P.err, err);
-            return;
-        }
+        for (int i = 0; i < 2; ++i)
+            if (ends[i].off) ends[i].before += ends[i].chunks - max(ends[i].off - kSplitUnitCost, 0);
     }
-    const int share = x1 - x0;  // indexes from here on count from the share's first chunk
+    const int share = ends[1].before - ends[0].before;  // chunks; indexes from here on count from the first of them
+    if (share <= 0) {
+        report(P.err, err);
+        return;
+    }
+    SplitPos ahead;  // of this warp's next chunk to copy
+    ahead.r = ends[0].r;
+    ahead.q = split_req(P, ahead.r);
+    ahead.head = ends[0].unit / ahead.q.tiles;
+    ahead.tile = ends[0].unit % ahead.q.tiles;
+    ahead.c = max(ends[0].off - kSplitUnitCost, 0);
+    if (aligned && ends[0].off) ahead.advance(P, ahead.q.chunks - ahead.c);
 
     // ---- this warp's copies, up to two chunks ahead of its computation
     int ax = 0;         // index of `ahead`
@@ -806,7 +833,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
                     }
                 } else {
                     // the share starts inside this unit: its part, of those of CTAs first .. last (this one)
-                    const int first = shares.owner(x0 + cx - at.c), last = blockIdx.x;
+                    const int first = shares.owner(unit0 + kSplitUnitCost), last = blockIdx.x;
                     float *p = static_cast<float *>(A.workspace) + P.ws_parts +
                                2ull * blockIdx.x * split_partial_floats<D>();
 #pragma unroll
@@ -865,7 +892,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     if (in_last) split_put<D>(results + warp * kResult, lane, U);
     __syncthreads();
     const bool whole_unit = n_last == last.q.chunks;
-    const int u0 = x0 + share - 1 - last.c;
+    const int u0 = (s0 > 0 ? unit1 : unit0) + kSplitUnitCost;  // place of the unit's first chunk
     const int first = whole_unit ? 0 : shares.owner(u0), final = whole_unit ? 0 : shares.owner(u0 + last.q.chunks - 1);
     // a CTA's parts: of the unit that its share starts inside (0), and of the one that goes on in the next CTA's (1)
     auto part = [&](int cta, int first_cta) {
@@ -1646,9 +1673,11 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
                                   cudaStream_t s) {
     const AttnParams P = attn_params(c, a, err);
     int sms = 0;
-    // the split path counts chunks in 31 bits
+    // rows of a request, and the split path's places, are counted in 31 bits
+    if (static_cast<int64_t>(a.n_tokens) * P.group > INT32_MAX) return LaunchStatus::kUnsupported;
     const int64_t tiles = (std::min<int64_t>(static_cast<int64_t>(a.max_q_len) * P.group, kSplitMaxRows) + kSplitCols - 1) / kSplitCols;
-    const int64_t chunks = std::max<int64_t>(((static_cast<int64_t>(a.max_pages) << P.page_shift) + kSplitKeys - 1) / kSplitKeys, 1);
+    const int64_t chunks =
+        std::max<int64_t>(((static_cast<int64_t>(a.max_pages) << P.page_shift) + kSplitKeys - 1) / kSplitKeys, 1) + kSplitUnitCost;
     if (static_cast<double>(a.n_reqs) * P.kv_heads * tiles * chunks >= 2147483648.0) return LaunchStatus::kUnsupported;
     if (!prepare(&sms)) return LaunchStatus::kCuda;
     if (c.head_dim == 128) launch_split<128>(P, sms, s);
@@ -1658,7 +1687,6 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
         // one of each request that has more rows than the other path takes
         const int64_t rows = static_cast<int64_t>(a.n_tokens) * P.group;
         const int64_t pairs = rows / (2 * kPrefillTile) + std::min<int64_t>(a.n_reqs, rows / (kSplitMaxRows + 1));
-        if (pairs > INT32_MAX) return LaunchStatus::kInvalid;
         const dim3 grid(static_cast<unsigned>(pairs), P.kv_heads);
         if (pairs == 0) return LaunchStatus::kOk;
         if (c.head_dim == 128) attention_prefill_kernel<128><<<grid, kPrefillThreads, kPrefillSmem<128>, s>>>(P);
