@@ -26,6 +26,7 @@ struct AttnParams {
     df11_kv4_attention_args a;
     int *err;
     uint64_t wait_ns;   // limit of each wait for a copy
+    int32_t parts;      // CTAs that share the keys of a pair of tiles (many rows)
     uint32_t ws_parts;  // workspace, in floats: counters before, partial results from here
 };
 
@@ -60,6 +61,13 @@ template <int D>
 __host__ __device__ constexpr uint32_t split_partial_floats() {
     return kSplitCols * D + 2 * kSplitCols;
 }
+
+// The many-row kernel may start while the few-row one, launched before it, still
+// runs: neither reads what the other writes.  The few-row kernel lets it, and
+// its first CTA waits for that one's end, so what follows in the stream follows
+// both.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The part of a request that this path handles: chunks [c_lo, c_lo + chunks)
 // of its keys for each of `units` (cache head, tile of 8 rows) pairs.  A
@@ -641,6 +649,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     const df11_kv4_attention_args &A = P.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t err = 0;
+    grid_release();
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < kSplitStages; ++i) mbar_init(&S.full[warp][i], 1);
@@ -994,6 +1003,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
 // sets a flag that ends the others.
 constexpr int kPrefillThreads = 512;
 constexpr int kPrefillTile = 128;  // rows of a tile, keys of a step
+constexpr int kPrefillParts = 8;   // CTAs of a cluster that share a pair's keys, at most
+// Steps of a pair that one CTA takes alone: a join takes as long as 3 (D = 64)
+// to 5 (D = 128) steps, most of it the transfer between the CTAs' shared memories.
+constexpr int kPrefillAlone = 6;
+constexpr int kPrefillSort = 64;   // requests that are put in order of their keys, at most
 constexpr float kLazy = 8.0f;      // log2 units a row's maximum may grow before O is rescaled
 
 template <int D>
@@ -1004,8 +1018,13 @@ struct PrefillShared {
     uint8_t k[2][kOperand], v[2][kOperand];
     alignas(16) uint32_t ok[4][4];  // keys of a step that are there; the softmax may read a step's while the next two are decoded
     float row[2][kPrefillTile];  // factor of a row's scores
+    union {
+        float2 part[2 * kPrefillTile];  // (m, l) of a row, where CTAs share its keys
+        int2 list[kPrefillThreads];     // (keys, pairs of tiles) of requests, before that
+    };
     uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], end;
     int32_t sums[kPrefillThreads / 32];
+    uint32_t some[kPrefillThreads / 32];
     uint32_t tmem, abort;
     int32_t req, pair;
 };
@@ -1024,6 +1043,41 @@ __device__ __forceinline__ uint32_t swz128_desc_low(uint32_t saddr) { return ((s
 __device__ __forceinline__ uint64_t swz128_desc(uint32_t low) {
     return static_cast<uint64_t>(low) | (static_cast<uint64_t>((1024u >> 4) | (1u << 14) | (2u << 29)) << 32);
 }
+
+// The CTAs of a cluster.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// All of the CTA's warps, wherever each is.
+__device__ __forceinline__ void prefill_sync() { asm volatile("barrier.sync 1, %0;" ::"n"(kPrefillThreads) : "memory"); }
 
 template <class Shared>
 __device__ __forceinline__ bool prefill_wait_slow(uint64_t *bar, uint32_t parity, Shared &S, uint64_t limit_ns) {
@@ -1060,6 +1114,12 @@ __device__ __forceinline__ int prefill_pairs(const AttnParams &P, int r) {
     if (!rows_valid(P.a, q0, q1)) return 0;
     const int64_t rows = static_cast<int64_t>(q1 - q0) * P.group;
     return rows > kSplitMaxRows ? static_cast<int>((rows + 2 * kPrefillTile - 1) / (2 * kPrefillTile)) : 0;
+}
+
+// The most keys that rows of a tile see, nearly: what its time goes with.
+__device__ __forceinline__ int prefill_keys(const AttnParams &P, int r) {
+    const int kv = __ldg(P.a.kv_lens + r);
+    return P.a.window ? min(kv, P.a.window) : kv;
 }
 
 // Keys [lo, hi) that row `row` of the request sees.
@@ -1103,53 +1163,153 @@ __device__ __forceinline__ PrefillWork prefill_work(const AttnParams &P, int req
     return W;
 }
 
+// Part `part` of the pair's steps, of equal ones.
+__device__ __forceinline__ void prefill_part(PrefillWork &W, int part, int parts) {
+    const int per = (W.steps + parts - 1) / parts, s0 = min(part * per, W.steps), s1 = min(s0 + per, W.steps);
+    W.first += s0;
+    W.steps = s1 - s0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        W.a0[x] = max(W.a0[x] - s0, 0);
+        W.a1[x] = min(W.a1[x] - s0, W.steps);
+        if (W.a0[x] >= W.a1[x]) W.a0[x] = W.a1[x] = 0;
+    }
+}
+
+// Joins the parts of rows [rank * 256 / PARTS, ...) of the pair, which the
+// CTAs of the cluster hold in shared memory: O in FP32 at `o`, a row's 16-byte
+// chunks xored with its number's last 3 bits, and (m, l) at `ml`.  16 chunks
+// of a thread's rows are in flight together.
+template <int D, int PARTS>
+__device__ __forceinline__ void prefill_join(const AttnParams &P, const PrefillWork &W, int head, int warp, int lane,
+                                             uint32_t o, uint32_t ml) {
+    const df11_kv4_attention_args &A = P.a;
+    constexpr int kLanes = D / 4, kAt = 32 / kLanes;  // lanes of a row; rows at a time
+    constexpr int kRows = 2 * kPrefillTile / PARTS, kBatch = 16 / PARTS;
+    const int group = static_cast<int>(P.group), c = lane % kLanes;
+    const int first = static_cast<int>(cluster_rank()) * kRows + lane / kLanes;
+    uint32_t from_o[PARTS], from_ml[PARTS];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) from_o[p] = cluster_addr(o, p), from_ml[p] = cluster_addr(ml, p);
+#pragma unroll 1
+    for (int i = warp * kAt; i < kRows; i += 8 * kAt * kBatch) {
+        float2 s[kBatch][PARTS];
+        float4 v[kBatch][PARTS];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int r = first + min(i + 8 * kAt * b, kRows - kAt);
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                s[b][p] = cluster_ld2(from_ml[p] + r * 8);
+                v[b][p] = cluster_ld4(from_o[p] + (r * D + 4 * (c ^ (r & 7))) * 4);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int row = W.row0 + first + i + 8 * kAt * b;
+            if (i + 8 * kAt * b >= kRows || row >= W.rows) continue;
+            float top = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) top = fmaxf(top, s[b][p].x);
+            const float shift = top == -INFINITY ? 0.0f : top;
+            float l = 0.0f, x[4] = {};
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                if (s[b][p].y == 0.0f) continue;  // no key of this part was seen, and its O may be anything
+                const float h = ex2(s[b][p].x - shift);
+                l += s[b][p].y * h;
+                x[0] += v[b][p].x * h, x[1] += v[b][p].y * h, x[2] += v[b][p].z * h, x[3] += v[b][p].w * h;
+            }
+            const float inv = l > 0.0f ? P.v_scale / l : l;  // NaN stays NaN
+            const int64_t token = W.q0 + row / group;
+            const int hq = head * group + row % group;
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.o) + token * static_cast<int64_t>(A.o_token_stride) + hq * D +
+                                       4 * c) = make_uint2(bf16x2_of(x[0] * inv, x[1] * inv), bf16x2_of(x[2] * inv, x[3] * inv));
+            if (A.lse && c == 0) A.lse[token * A.n_q_heads + hq] = lse_of(top, l);
+        }
+    }
+}
+
 // The block-table entry of key `key`, or kNoPage where the page holds no key a row sees.
 __device__ __forceinline__ int64_t prefill_page(const AttnParams &P, const PrefillWork &W, int64_t key) {
     if (key >= W.end || (((key >> P.page_shift) + 1) << P.page_shift) <= W.begin) return kNoPage;
     return __ldg(P.a.block_table + static_cast<int64_t>(W.req) * P.a.max_pages + (key >> P.page_shift));
 }
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(const AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     PrefillShared<D> &S =
         *reinterpret_cast<PrefillShared<D> *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
     const df11_kv4_attention_args &A = P.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int head = blockIdx.y, group = static_cast<int>(P.group);
+    const int group = static_cast<int>(P.group);
 
-    // ---- this CTA's request and rows: pairs of tiles counted over the
-    // requests; the last rows first, which see the most keys
-    {
-        int all = 0, want = -1;
-        for (int pass = 0; pass < 2; ++pass) {
-            int base = 0;
-            for (int b = 0; b < A.n_reqs; b += kPrefillThreads) {
-                const int w = prefill_pairs(P, b + tid);
-                int incl = w;
+    // ---- this CTA's request and rows: pairs of tiles in the order of the most
+    // keys that a row of the request sees, a request's last rows first (the
+    // last to start should not be long: 9 ragged requests take XX us so, and
+    // XX in order of the requests)
+    const uint32_t place = SHARED ? blockIdx.x / P.parts : blockIdx.x;
+    const int want = static_cast<int>(place / P.kv_heads), head = static_cast<int>(place % P.kv_heads);
+    int all = 0, many = 0;
+    for (int b = 0; b < A.n_reqs; b += kPrefillThreads) {
+        const int w = prefill_pairs(P, b + tid);
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, w > 0);
+        const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w));
+        __syncthreads();
+        if (lane == 0) {
+            S.sums[warp] = static_cast<int32_t>(sum);
+            S.some[warp] = mask;
+        }
+        S.list[tid] = make_int2(w ? prefill_keys(P, b + tid) : 0, w);
+        __syncthreads();
+        for (int i = 0; i < kPrefillThreads / 32; ++i) {
+            all += S.sums[i];
+            many += __popc(S.some[i]);
+        }
+    }
+    if (want >= all) {
+        if (blockIdx.x == 0) grid_wait();
+        return;
+    }
+    if (A.n_reqs <= kPrefillThreads && many <= kPrefillSort) {
+        const int2 mine = S.list[tid];
+        int at = 0;
+        if (mine.y)
+            for (int i = 0; i < kPrefillThreads / 32; ++i)
+                for (uint32_t m = S.some[i]; m; m &= m - 1) {
+                    const int j = 32 * i + __ffs(m) - 1;
+                    const int2 other = S.list[j];
+                    if (other.x > mine.x || (other.x == mine.x && j > tid)) at += other.y;
+                }
+        if (mine.y && at <= want && want < at + mine.y) {
+            S.req = tid;
+            S.pair = mine.y - 1 - (want - at);
+        }
+    } else {
+        // in the order of the requests, from the last
+        int base = 0;
+        const int from = all - 1 - want;
+        for (int b = 0; b < A.n_reqs; b += kPrefillThreads) {
+            const int w = prefill_pairs(P, b + tid);
+            int incl = w;
 #pragma unroll
-                for (int x = 1; x < 32; x <<= 1) {
-                    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, x);
-                    if (lane >= x) incl += o;
-                }
-                __syncthreads();
-                if (lane == 31) S.sums[warp] = incl;
-                __syncthreads();
-                int before = base;
-                for (int i = 0; i < kPrefillThreads / 32; ++i) {
-                    if (i < warp) before += S.sums[i];
-                    base += S.sums[i];
-                }
-                const int at = before + incl - w;
-                if (pass && w && at <= want && want < at + w) {
-                    S.req = b + tid;
-                    S.pair = want - at;
-                }
+            for (int x = 1; x < 32; x <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, incl, x);
+                if (lane >= x) incl += o;
             }
-            if (!pass) {
-                all = base;
-                want = all - 1 - static_cast<int>(blockIdx.x);
-                if (want < 0) return;
+            __syncthreads();
+            if (lane == 31) S.sums[warp] = incl;
+            __syncthreads();
+            int before = base;
+            for (int i = 0; i < kPrefillThreads / 32; ++i) {
+                if (i < warp) before += S.sums[i];
+                base += S.sums[i];
+            }
+            const int at = before + incl - w;
+            if (w && at <= from && from < at + w) {
+                S.req = b + tid;
+                S.pair = from - at;
             }
         }
     }
@@ -1176,7 +1336,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    const PrefillWork W = prefill_work(P, S.req, S.pair);
+    PrefillWork W = prefill_work(P, S.req, S.pair);
+    const bool shared = SHARED && W.steps > kPrefillAlone;
+    const int part = SHARED ? static_cast<int>(blockIdx.x) % P.parts : 0;
+    if constexpr (SHARED) prefill_part(W, part, shared ? P.parts : 1);
     uint32_t err = 0;
 
     if (warp < 8) {
@@ -1189,7 +1352,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
         const int hq = head * group + row % group;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's TMEM lanes
         const uint32_t s_col = tmem + lanes + x * kPrefillTile, o_col = tmem + lanes + 2 * kPrefillTile + x * D;
-        const int steps = W.a1[x] - W.a0[x];
+        const int a0 = x ? W.a0[1] : W.a0[0], steps = (x ? W.a1[1] : W.a1[0]) - a0;
         float f = 0.0f;
         if (steps) {
             // The warp's 32 rows of queries, a row's 16-byte chunks on D / 8 lanes,
@@ -1238,19 +1401,20 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
             fence_proxy_async_smem();
             mbar_arrive(&S.q_full[x]);
         }
-        // keys [lo, hi) seen by this row, from the tile's first step on
+        // keys [lo, hi) seen by this row, from the tile's first step on; rows past
+        // the last (zeros) as that one: they must not make every step a masked one
         int lo = 0, hi = 0;
-        if (live) {
+        {
             int64_t lo64, hi64;
-            prefill_row(P, W, row, lo64, hi64);
-            const int64_t from = static_cast<int64_t>(W.first + W.a0[x]) * kPrefillTile;
+            prefill_row(P, W, min(row, W.rows - 1), lo64, hi64);
+            const int64_t from = static_cast<int64_t>(W.first + a0) * kPrefillTile;
             lo = static_cast<int>(max(lo64 - from, static_cast<int64_t>(0)));
             hi = static_cast<int>(max(hi64 - from, static_cast<int64_t>(0)));
         }
         float m = -INFINITY, l = 0.0f;
         bool run = true;
         for (int it = 0; it < steps; ++it) {
-            const int j = W.a0[x] + it;
+            const int j = a0 + it;
             run = __all_sync(0xFFFFFFFFu, prefill_wait(&S.s_full[x], it & 1u, S, P.wait_ns));
             if (!run) break;
             tc_fence_after();
@@ -1339,10 +1503,35 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
             tc_fence_after();
         }
         if (!run) err |= DF11_DEV_ERR_TIMEOUT;
+        if (shared) {
+            // the part's rows to shared memory, where no MMA reads any more
+            prefill_sync();
+            float *o = reinterpret_cast<float *>(S.q[0]);
+            const int at = x * kPrefillTile + r;
+            if (!run || !steps) m = -INFINITY, l = 0.0f;
+            S.part[at] = make_float2(m, l);
+            if (run && steps) {
+#pragma unroll
+                for (int i = 0; i < D; i += 16) {
+                    uint32_t v[16];
+                    tc_ld16(o_col + i, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int y = 0; y < 16; y += 4)
+                        *reinterpret_cast<uint4 *>(o + at * D + 4 * (((i + y) / 4) ^ (at & 7))) =
+                            make_uint4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+                }
+            }
+            cluster_sync();
+            const uint32_t so = smem_addr(o), sp = smem_addr(S.part);
+            if (P.parts == 8) prefill_join<D, 8>(P, W, head, warp, lane, so, sp);
+            else if (P.parts == 4) prefill_join<D, 4>(P, W, head, warp, lane, so, sp);
+            else prefill_join<D, 2>(P, W, head, warp, lane, so, sp);
+            cluster_sync();
+        } else if (part == 0) {
         // Rows out of TMEM into the tile's query operand, which no MMA reads any
         // more (a thread its own row), and from there to o, a row's chunks on
         // D / 8 lanes.  l == 0: the row saw no key, whatever the accumulator holds.
-        if (m == -INFINITY) l = 0.0f;
         const float inv = !run ? 0.0f : l > 0.0f ? P.v_scale / l : l;  // NaN stays NaN
         if (steps) {
 #pragma unroll
@@ -1381,6 +1570,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
             }
         }
         if (live && A.lse) A.lse[token * A.n_q_heads + hq] = lse_of(m, l);
+        }
         tc_fence_before();
     } else if (warp < 12) {
         // =============================== the cache to FP16 operand tiles
@@ -1590,8 +1780,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
         }
         __syncwarp();
     }
+    if (shared && warp >= 8) {
+        prefill_sync();
+        cluster_sync();
+        cluster_sync();
+    }
     err = __reduce_or_sync(0xFFFFFFFFu, err);
     if (lane == 0) report(P.err, err);
+    if (blockIdx.x == 0) grid_wait();
     __syncthreads();
     if (warp == 12) {
         tc_fence_after();
@@ -1615,6 +1811,7 @@ AttnParams attn_params(const df11_kv4_cache &c, const df11_kv4_attention_args &a
     P.a = a;
     P.err = err;
     P.wait_ns = 2000000000ull;
+    P.parts = 1;
     P.ws_parts = kMaxCtas;
     return P;
 }
@@ -1631,15 +1828,57 @@ void launch_split(const AttnParams &P, int ctas, cudaStream_t s) {
 
 template <int D>
 constexpr size_t kPrefillSmem = sizeof(PrefillShared<D>) + 1024;  // and what aligns it
+static_assert(3 * 2 * PrefillShared<64>::kOperand >= 2 * kPrefillTile * 64 * 4 && 3 * 2 * PrefillShared<128>::kOperand >= 2 * kPrefillTile * 128 * 4,
+              "a part's rows fit the operands' place");
 
-bool prepare(int *sms) {
+template <int D>
+cudaError_t launch_prefill(const AttnParams &P, unsigned pairs, bool early, cudaStream_t s) {
+    cudaLaunchAttribute attrs[2]{};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(pairs * P.kv_heads * P.parts);
+    cfg.blockDim = dim3(kPrefillThreads);
+    cfg.dynamicSmemBytes = kPrefillSmem<D>;
+    cfg.stream = s;
+    cfg.attrs = attrs;
+    if (early) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (P.parts > 1) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[cfg.numAttrs++].val.clusterDim = {static_cast<unsigned>(P.parts), 1, 1};
+    }
+    return cudaLaunchKernelEx(&cfg, P.parts > 1 ? attention_prefill_kernel<D, true> : attention_prefill_kernel<D, false>, P);
+}
+
+// Clusters of `parts` prefill CTAs that run at the same time.
+int max_clusters(int parts) {
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim = {static_cast<unsigned>(parts), 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(parts);
+    cfg.blockDim = dim3(kPrefillThreads);
+    cfg.dynamicSmemBytes = kPrefillSmem<128>;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, attention_prefill_kernel<128, true>, &cfg) == cudaSuccess ? n : 0;
+}
+
+struct Device {
+    int sms = 0;
+    int clusters[4] = {};  // of 1 << i prefill CTAs, at the same time
+};
+
+bool prepare(Device *d) {
     constexpr int kDevices = 64;
     static std::mutex mu;
-    static int known[kDevices] = {};
+    static Device known[kDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return false;
     std::lock_guard<std::mutex> lk(mu);
-    if (!known[dev]) {
+    if (!known[dev].sms) {
         int v = 0;
         if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
         auto allow = [](auto *kernel, size_t bytes) {
@@ -1652,12 +1891,15 @@ bool prepare(int *sms) {
             !allow(&attention_split_kernel<128, 4>, sizeof(SplitShared<128>)) ||
             !allow(&attention_split_kernel<128, 5>, sizeof(SplitShared<128>)) ||
             !allow(&attention_split_kernel<128, 6>, sizeof(SplitShared<128>)) ||
-            !allow(&attention_prefill_kernel<64>, kPrefillSmem<64>) ||
-            !allow(&attention_prefill_kernel<128>, kPrefillSmem<128>))
+            !allow(&attention_prefill_kernel<64, false>, kPrefillSmem<64>) ||
+            !allow(&attention_prefill_kernel<64, true>, kPrefillSmem<64>) ||
+            !allow(&attention_prefill_kernel<128, false>, kPrefillSmem<128>) ||
+            !allow(&attention_prefill_kernel<128, true>, kPrefillSmem<128>))
             return false;
-        known[dev] = v;
+        for (int i = 1; 1 << i <= kPrefillParts; ++i) known[dev].clusters[i] = max_clusters(1 << i);
+        known[dev].sms = std::min(v, kMaxCtas);
     }
-    *sms = known[dev] < kMaxCtas ? known[dev] : kMaxCtas;
+    *d = known[dev];
     return true;
 }
 
@@ -1671,26 +1913,37 @@ LaunchStatus kv4_attention_workspace(const df11_kv4_cache &c, const df11_kv4_att
 
 LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attention_args &a, int *err,
                                   cudaStream_t s) {
-    const AttnParams P = attn_params(c, a, err);
-    int sms = 0;
-    // rows of a request, and the split path's places, are counted in 31 bits
-    if (static_cast<int64_t>(a.n_tokens) * P.group > INT32_MAX) return LaunchStatus::kUnsupported;
+    AttnParams P = attn_params(c, a, err);
+    Device dev;
+    // rows, and the split path's places, are counted in 31 bits
+    if (static_cast<int64_t>(a.n_tokens) * a.n_q_heads > INT32_MAX) return LaunchStatus::kUnsupported;
     const int64_t tiles = (std::min<int64_t>(static_cast<int64_t>(a.max_q_len) * P.group, kSplitMaxRows) + kSplitCols - 1) / kSplitCols;
     const int64_t chunks =
         std::max<int64_t>(((static_cast<int64_t>(a.max_pages) << P.page_shift) + kSplitKeys - 1) / kSplitKeys, 1) + kSplitUnitCost;
     if (static_cast<double>(a.n_reqs) * P.kv_heads * tiles * chunks >= 2147483648.0) return LaunchStatus::kUnsupported;
-    if (!prepare(&sms)) return LaunchStatus::kCuda;
-    if (c.head_dim == 128) launch_split<128>(P, sms, s);
-    else launch_split<64>(P, sms, s);
+    if (!prepare(&dev)) return LaunchStatus::kCuda;
+    if (c.head_dim == 128) launch_split<128>(P, dev.sms, s);
+    else launch_split<64>(P, dev.sms, s);
     if (static_cast<int64_t>(a.max_q_len) * P.group > kSplitMaxRows) {
-        // as many pairs of tiles as the rows can make: full ones, and a last
-        // one of each request that has more rows than the other path takes
+        // as many pairs of tiles as the rows can make, the last one of each
+        // request that has more rows than the other path takes with one row
         const int64_t rows = static_cast<int64_t>(a.n_tokens) * P.group;
-        const int64_t pairs = rows / (2 * kPrefillTile) + std::min<int64_t>(a.n_reqs, rows / (kSplitMaxRows + 1));
-        const dim3 grid(static_cast<unsigned>(pairs), P.kv_heads);
-        if (pairs == 0) return LaunchStatus::kOk;
-        if (c.head_dim == 128) attention_prefill_kernel<128><<<grid, kPrefillThreads, kPrefillSmem<128>, s>>>(P);
-        else attention_prefill_kernel<64><<<grid, kPrefillThreads, kPrefillSmem<64>, s>>>(P);
+        const int64_t some = std::min<int64_t>(a.n_reqs, rows / (kSplitMaxRows + 1));
+        const int64_t pairs = (rows + some * (2 * kPrefillTile - 1)) / (2 * kPrefillTile);
+        if (some == 0) return LaunchStatus::kOk;
+        // where clusters of CTAs, one for each pair and head, run all at the same
+        // time, they share the keys: 85 tokens in groups of 3 against 8192 keys of
+        // 8 heads take 154 us alone (D = 64; 168 for D = 128), XX (XX) with 8
+        const int64_t steps = ((static_cast<int64_t>(a.max_pages) << P.page_shift) + kPrefillTile - 1) / kPrefillTile;
+        for (int i = 1; 1 << i <= kPrefillParts && steps > kPrefillAlone; ++i)
+            if (pairs * P.kv_heads <= dev.clusters[i]) P.parts = 1 << i;
+        // a launch of up to two CTAs a multiprocessor starts while the first
+        // kernel runs (9 ragged requests: 65 us, not 71); a larger one is
+        // slower that way (a prompt of 8192 tokens: 554 us, not 543)
+        const bool early = pairs * P.kv_heads * P.parts <= 2 * dev.sms;
+        const cudaError_t e = c.head_dim == 128 ? launch_prefill<128>(P, static_cast<unsigned>(pairs), early, s)
+                                                : launch_prefill<64>(P, static_cast<unsigned>(pairs), early, s);
+        if (e != cudaSuccess) return LaunchStatus::kCuda;
     }
     return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;
 }

@@ -805,9 +805,9 @@ uint64_t df11_kv4_attention_workspace_bytes(const df11_kv4_cache *cache, const d
  * q_start descending or past n_tokens, or a request longer than max_q_len
  * (those rows are not written).
  * Errors: DF11_EINVAL, DF11_EUNSUPPORTED (head_dim, page_size, or a call too
- * large for 31-bit counts, which has to be split: n_tokens * n_q_heads /
- * n_heads rows, or the product of n_reqs, n_heads, tiles of 8 of a request's
- * first 64 rows, and 16 more than max_pages holds chunks of 64 keys),
+ * large for 31-bit counts, which has to be split: n_tokens * n_q_heads,
+ * or the product of n_reqs, n_heads, tiles of 8 of a request's first 64 rows,
+ * and 16 more than max_pages holds chunks of 64 keys),
  * DF11_ENOMEM (workspace too small), DF11_ECUDA. */
 df11_status df11_kv4_attention(const df11_kv4_cache *cache, const df11_kv4_attention_args *args, int *dev_err_flag,
                                df11_stream stream);

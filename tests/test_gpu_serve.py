@@ -516,6 +516,37 @@ def test_score_ranges(df11, n):
         p.check(o, lse, scale=scale)
 
 
+@pytest.mark.parametrize("hq,h,d", [(4, 1, 128), (4, 1, 64), (9, 3, 64), (16, 4, 128), (24, 8, 64), (7, 7, 128)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 333), (True, 5), (False, 0)])
+def test_prompts_over_long_contexts(df11, hq, h, d, causal, window):
+    """Few rows against many keys, which several CTAs share: short last tiles, parts without a step, rows that see
+    keys of one part only or none at all."""
+    lens = [(90, 3000)] if h < 7 else [(90, 3000), (300, 1025)]
+    for lens in (lens, [(257, 257)], [(200, 1300), (1, 800), (100, 30), (129, 385)], [(100, 0), (131, 2047)]):
+        p = Problem(df11, lens, hq, h, d, 32, seed=hq)
+        o, lse, err = p.run(causal=causal, window=window)
+        assert err.item() == 0
+        p.check(o, lse, causal=causal, window=window)
+        o2, lse2, _ = p.run(causal=causal, window=window)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lens", [[(1, 900), (2, 300)], [(300, 300), (70, 2500)], [(1100, 1100)] * 3])
+def test_nan_queries(df11, lens):
+    """A NaN in a head's query makes that row NaN and leaves every other as it is."""
+    p = Problem(df11, lens, 8, 4, 64, 16)
+    o, lse, _ = p.run()
+    rows = sorted({0, int(p.starts[1]) - 1, int(p.starts[-1]) - 1})
+    for t in rows:
+        p.q[t, 3 * 64 + 5] = float("nan")
+    o2, lse2, err = p.run()
+    assert err.item() == 0
+    for t in rows:
+        assert torch.isnan(o2[t, 192:256].float()).all() and torch.isnan(lse2[t, 3])
+        o2[t, 192:256], lse2[t, 3] = o[t, 192:256], lse[t, 3]
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_split_scales(df11):
     """Cache scales that are no powers of two."""
     p = Problem(df11, [(1, 1000), (70, 300)], 4, 2, 64, 32, gk=0.37, gv=1.9)

@@ -164,7 +164,7 @@ def test_attention_refusals(df11):
         df11.df11_kv4_attention(c, **{**good, **b})
     for b in [(0, 2, 5, 3), (3, 2, 5, 3), (4, -1, 5, 3), (4, 2, -1, 3), (4, 2, 5, -1)]:
         assert df11.df11_kv4_attention_workspace_bytes(c, *b) == 0
-    # past 31 bits: 2 ** 30 rows of a group of 2; 2 ** 16 requests x 2 heads x 8 tiles of rows x (2 ** 13 * 16 / 64 + 16)
+    # past 31 bits: 2 ** 30 tokens of 4 heads; 2 ** 16 requests x 2 heads x 8 tiles of rows x (2 ** 13 * 16 / 64 + 16)
     # chunks; 2 ** 28 x 2 x 1 x (1 + 16)
     for b in [dict(n_tokens=1 << 30), dict(n_reqs=1 << 16, max_q_len=32, max_pages=1 << 13),
               dict(n_reqs=1 << 28, max_pages=0)]:
