@@ -27,6 +27,7 @@ struct AttnParams {
     int *err;
     uint64_t wait_ns;   // limit of each wait for a copy
     int32_t parts;      // CTAs that share the keys of a pair of tiles (many rows)
+    bool early;         // the many-row kernel may start before the few-row one has ended
     uint32_t ws_parts;  // workspace, in floats: counters before, partial results from here
 };
 
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     const df11_kv4_attention_args &A = P.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t err = 0;
-    grid_release();
+    if (P.early) grid_release();
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < kSplitStages; ++i) mbar_init(&S.full[warp][i], 1);
@@ -1251,7 +1252,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
     // 209 to 7278 keys take 49 us so, and 60 in the order of the requests)
     const uint32_t place = SHARED ? blockIdx.x / P.parts : blockIdx.x;
     const int want = static_cast<int>(place / P.kv_heads), head = static_cast<int>(place % P.kv_heads);
-    int all = 0, many = 0;
+    int64_t all = 0;  // 64 bits: row starts that are no ascending ones could count the same rows many times
+    int many = 0;
     for (int b = 0; b < A.n_reqs; b += kPrefillThreads) {
         const int w = prefill_pairs(P, b + tid);
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, w > 0);
@@ -1288,8 +1290,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
         }
     } else {
         // in the order of the requests, from the last
-        int base = 0;
-        const int from = all - 1 - want;
+        int64_t base = 0;
+        const int64_t from = all - 1 - want;
         for (int b = 0; b < A.n_reqs; b += kPrefillThreads) {
             const int w = prefill_pairs(P, b + tid);
             int incl = w;
@@ -1301,15 +1303,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
             __syncthreads();
             if (lane == 31) S.sums[warp] = incl;
             __syncthreads();
-            int before = base;
+            int64_t before = base;
             for (int i = 0; i < kPrefillThreads / 32; ++i) {
                 if (i < warp) before += S.sums[i];
                 base += S.sums[i];
             }
-            const int at = before + incl - w;
+            const int64_t at = before + incl - w;
             if (w && at <= from && from < at + w) {
                 S.req = b + tid;
-                S.pair = from - at;
+                S.pair = static_cast<int32_t>(from - at);
             }
         }
     }
@@ -1832,7 +1834,7 @@ static_assert(3 * 2 * PrefillShared<64>::kOperand >= 2 * kPrefillTile * 64 * 4 &
               "a part's rows fit the operands' place");
 
 template <int D>
-cudaError_t launch_prefill(const AttnParams &P, unsigned pairs, bool early, cudaStream_t s) {
+cudaError_t launch_prefill(const AttnParams &P, unsigned pairs, cudaStream_t s) {
     cudaLaunchAttribute attrs[2]{};
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(pairs * P.kv_heads * P.parts);
@@ -1840,7 +1842,7 @@ cudaError_t launch_prefill(const AttnParams &P, unsigned pairs, bool early, cuda
     cfg.dynamicSmemBytes = kPrefillSmem<D>;
     cfg.stream = s;
     cfg.attrs = attrs;
-    if (early) {
+    if (P.early) {
         attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
@@ -1863,7 +1865,9 @@ int max_clusters(int parts) {
     cfg.attrs = &cluster;
     cfg.numAttrs = 1;
     int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, attention_prefill_kernel<128, true>, &cfg) == cudaSuccess ? n : 0;
+    if (cudaOccupancyMaxActiveClusters(&n, attention_prefill_kernel<128, true>, &cfg) == cudaSuccess) return n;
+    cudaGetLastError();  // they then share no keys
+    return 0;
 }
 
 struct Device {
@@ -1922,27 +1926,29 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
         std::max<int64_t>(((static_cast<int64_t>(a.max_pages) << P.page_shift) + kSplitKeys - 1) / kSplitKeys, 1) + kSplitUnitCost;
     if (static_cast<double>(a.n_reqs) * P.kv_heads * tiles * chunks >= 2147483648.0) return LaunchStatus::kUnsupported;
     if (!prepare(&dev)) return LaunchStatus::kCuda;
-    if (c.head_dim == 128) launch_split<128>(P, dev.sms, s);
-    else launch_split<64>(P, dev.sms, s);
+    int64_t pairs = 0;
     if (static_cast<int64_t>(a.max_q_len) * P.group > kSplitMaxRows) {
         // as many pairs of tiles as the rows can make, the last one of each
         // request that has more rows than the other path takes with one row
         const int64_t rows = static_cast<int64_t>(a.n_tokens) * P.group;
         const int64_t some = std::min<int64_t>(a.n_reqs, rows / (kSplitMaxRows + 1));
-        const int64_t pairs = (rows + some * (2 * kPrefillTile - 1)) / (2 * kPrefillTile);
-        if (some == 0) return LaunchStatus::kOk;
+        pairs = (rows + some * (2 * kPrefillTile - 1)) / (2 * kPrefillTile);
         // where clusters of CTAs, one for each pair and head, run all at the same
         // time, they share the keys: 85 tokens in groups of 3 against 8192 keys of
         // 8 heads take 154 us alone (D = 64; 168 for D = 128), 31 (38) with 8
         const int64_t steps = ((static_cast<int64_t>(a.max_pages) << P.page_shift) + kPrefillTile - 1) / kPrefillTile;
-        for (int i = 1; 1 << i <= kPrefillParts && steps > kPrefillAlone; ++i)
+        for (int i = 1; pairs && 1 << i <= kPrefillParts && steps > kPrefillAlone; ++i)
             if (pairs * P.kv_heads <= dev.clusters[i]) P.parts = 1 << i;
         // a launch of up to two CTAs a multiprocessor starts while the first
         // kernel runs (9 ragged requests: 65 us, not 71); a larger one is
         // slower that way (a prompt of 8192 tokens: 554 us, not 543)
-        const bool early = pairs * P.kv_heads * P.parts <= 2 * dev.sms;
-        const cudaError_t e = c.head_dim == 128 ? launch_prefill<128>(P, static_cast<unsigned>(pairs), early, s)
-                                                : launch_prefill<64>(P, static_cast<unsigned>(pairs), early, s);
+        P.early = pairs && pairs * P.kv_heads * P.parts <= 2 * dev.sms;
+    }
+    if (c.head_dim == 128) launch_split<128>(P, dev.sms, s);
+    else launch_split<64>(P, dev.sms, s);
+    if (pairs) {
+        const cudaError_t e = c.head_dim == 128 ? launch_prefill<128>(P, static_cast<unsigned>(pairs), s)
+                                                : launch_prefill<64>(P, static_cast<unsigned>(pairs), s);
         if (e != cudaSuccess) return LaunchStatus::kCuda;
     }
     return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;

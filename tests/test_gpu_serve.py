@@ -688,6 +688,82 @@ def test_graph_replays_with_other_lengths(df11):
             assert ((got[0][r:r + 1].double().cpu().reshape(1, 8, 128) - wo).abs() <= bo).all()
 
 
+def test_graph_replays_a_mixed_batch(df11):
+    """Both kernels in one captured call, replayed with other lengths: rows go from one kernel to the other, requests
+    lose all their rows or keys, and what follows in the graph reads what both have written."""
+    lens = [(90, 1200), (4, 900), (40, 700), (1, 1300)]
+    p = Problem(df11, lens, 8, 2, 64, 16, tail=0)
+    t, hq, d = p.t, 8, 64
+    q = p.q[:, :hq * d].contiguous()
+    o, lse = torch.empty(t, hq * d, dtype=torch.bfloat16, device="cuda"), torch.empty(t, hq, device="cuda")
+    need = df11.df11_kv4_attention_workspace_bytes(p.handle, hq, 4, t, 90)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    qs, kl, tb, err = dev(p.starts, torch.int32), dev([kv for _, kv in lens], torch.int32), dev(p.table, torch.int32), word()
+
+    def call():
+        df11.df11_kv4_attention(p.handle, q.data_ptr(), hq * d, o.data_ptr(), hq * d, hq, qs.data_ptr(), kl.data_ptr(),
+                                tb.data_ptr(), 4, p.width, t, 90, d ** -0.5, ws.data_ptr(), need, lse_ptr=lse.data_ptr(),
+                                err_ptr=err.data_ptr(), stream=stream())
+        return o.float() * 2
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        twice = call()
+    for ns, kvs in (([90, 4, 40, 1], [1200, 900, 700, 1300]), ([4, 90, 1, 40], [1200, 900, 33, 1300]),
+                    ([0, 0, 0, 0], [5, 5, 5, 5]), ([17, 16, 90, 12], [0, 16, 90, 1]), ([1, 2, 3, 4], [1200, 900, 700, 1300])):
+        starts = np.concatenate([[0], np.cumsum(ns)])
+        qs.copy_(torch.tensor(starts, dtype=torch.int32))
+        kl.copy_(torch.tensor(kvs, dtype=torch.int32))
+        o.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(twice, o.float() * 2) and (o[starts[-1]:] == 7.0).all() and err.item() == 0
+        at = 0
+        for r, (n, kv) in enumerate(zip(ns, kvs)):
+            rows = slice(int(starts[r]), int(starts[r + 1]))
+            w = ref.attention(q[rows].double().cpu().reshape(n, hq, d), p.k[at:at + kv], p.v[at:at + kv], True, 0, d ** -0.5)
+            at += lens[r][1]
+            bo, _ = ref.attention_bounds(*w, kv, d)
+            assert ((o[rows].double().cpu().reshape(n, hq, d) - w[0]).abs() <= bo).all(), (r, n, kv)
+
+
+def test_more_prompts_than_are_sorted(df11):
+    """600 requests, 130 of them with more rows than the few-row kernel takes."""
+    g = np.random.default_rng(0)
+    lens = [(int(g.integers(17, 40)) if r % 5 == 3 else int(g.integers(0, 3)), int(g.integers(0, 90))) for r in range(600)]
+    lens[7] = (130, 500)
+    for some in (lens, lens[:300]):  # in two rounds of the CTA's threads, and in one
+        p = Problem(df11, some, 4, 1, 64, 16, seed=9)
+        o, lse, err = p.run()
+        assert err.item() == 0
+        p.check(o, lse)
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_no_pages(df11, n):
+    """A table without columns: requests without keys are zeros, others flagged; with no error word as well."""
+    p = Problem(df11, [(n, 0), (n, 0)], 4, 2, 64, 16)
+    q, o = p.q, torch.full((2 * n, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    need = df11.df11_kv4_attention_workspace_bytes(p.handle, 4, 2, 2 * n, n)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    qs = dev([0, n, 2 * n], torch.int32)
+    for kvs, want in (([0, 0], 0), ([0, 9], df11.DEV_ERR_PAGES)):
+        for err in (word(), None):
+            o.fill_(7.0)
+            kl = dev(kvs, torch.int32)
+            df11.df11_kv4_attention(p.handle, q.data_ptr(), q.shape[1], o.data_ptr(), 256, 4, qs.data_ptr(), kl.data_ptr(),
+                                    0, 2, 0, 2 * n, n, 0.125, ws.data_ptr(), need,
+                                    err_ptr=err.data_ptr() if err is not None else None, stream=stream())
+            torch.cuda.synchronize()
+            assert (o == 0).all() and (err is None or err.item() == want)
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits(df11):
     """A cache of 5 GB whose used pages lie at its end."""
