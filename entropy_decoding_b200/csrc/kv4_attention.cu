@@ -26,6 +26,7 @@ struct AttnParams {
     df11_kv4_attention_args a;
     int *err;
     uint64_t wait_ns;   // limit of each wait for a copy
+    int32_t split_rows; // a request's rows that the few-row kernel takes at most
     int32_t parts;      // CTAs that share the keys of a pair of tiles (many rows)
     bool early;         // the many-row kernel may start before the few-row one has ended
     uint32_t ws_parts;  // workspace, in floats: counters before, partial results from here
@@ -47,8 +48,13 @@ constexpr int kSplitThreads = 32 * kSplitWarps;
 constexpr int kSplitCols = 8;      // rows of a unit
 constexpr int kSplitKeys = 64;     // keys of a chunk: a warp's step
 constexpr int kSplitStages = 2;    // chunks that a warp has room for
-constexpr int kSplitMaxRows = 64;  // rows (tokens x heads of a group) of a request that go this way
-constexpr int kSplitAlign = 4 * kSplitWarps;  // units of at most so many chunks are not shared between CTAs
+// Rows (tokens x heads of a group) of a request that go this way at most: the
+// time goes with them in steps of 8, the other kernel's hardly.  32 requests on
+// 2000 keys of 8 heads of 128 take 86 us with 32 rows each, 131 with 48 and 165
+// with 64, the other kernel 90; one request alone 16 us with 32 to 64 rows, the
+// other kernel 23 (on 8000 keys: 19 to 29, and 34).
+constexpr int kSplitRows = 32, kSplitRowsFew = 64;
+constexpr int kSplitFew = 16;  // requests times cache heads, at most, with the second bound
 // What a unit costs a CTA beside its chunks (queries, joins), in chunks: shares
 // are equal in this measure, in which a unit starts with so many empty places.
 // 64 requests of 256 to 16384 keys (8 cache heads of 128, groups of 4) take 182 us
@@ -95,7 +101,7 @@ __device__ __forceinline__ SplitReq split_req(const AttnParams &P, int r) {
     if (!rows_valid(A, q.q0, q1)) return q;
     q.n = q1 - q.q0;
     const int64_t rows = static_cast<int64_t>(q.n) * P.group;
-    if (rows == 0 || rows > kSplitMaxRows) return q;
+    if (rows == 0 || rows > P.split_rows) return q;
     q.rows = static_cast<int32_t>(rows);
     q.tiles = (q.rows + kSplitCols - 1) / kSplitCols;
     q.kv = min(max(__ldg(A.kv_lens + r), 0), kMaxKeys);
@@ -630,6 +636,17 @@ __device__ __forceinline__ void split_put(float *at, int lane, const SplitUnit<D
     }
 }
 
+// Whether units of at most `longest` chunks are not divided between CTAs, whose
+// shares are of `share` places: units of a chunk a warp, and those that come
+// to about one or two a CTA.  A join of CTAs takes 1 to 3 us, and the last CTA to
+// finish has up to a unit more.  8 heads of 128: one token on 500 keys 10.1 us
+// whole, 11.2 divided; on 1000 12.9 and 11.5; 8 tokens on 1000 keys each 13.4
+// and 15.4, on 3000 20.6 and 19.0; 32 on 2000 28.8 and 31.5; 100 on 2000 82.6
+// and 80.4.
+__device__ __forceinline__ bool split_whole(int longest, int share) {
+    return longest <= kSplitWarps || (longest <= share + share / 4 && share <= 128);
+}
+
 // Persistent CTAs, each a contiguous, equal share of the launch's chunks
 // (request, unit, chunk in order), so a long request spreads over the GPU and
 // short ones share a CTA, whatever the mix.  A share's chunks go to the warps
@@ -640,8 +657,8 @@ __device__ __forceinline__ void split_put(float *at, int lane, const SplitUnit<D
 // joins them.  The share's last segment is joined by the whole CTA.  A unit
 // that spans CTAs goes through the workspace, and the CTA that arrives last
 // joins its parts at its own end, in order: no CTA waits for another, and the
-// result does not depend on which one was last.  Where all units are short
-// (kSplitAlign), a unit goes whole to the CTA whose share holds its first
+// result does not depend on which one was last.  Where units are short
+// (split_whole), a unit goes whole to the CTA whose share holds its first
 // chunk: fewer CTAs work, but none joins.
 template <int D, int ES>
 __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const AttnParams P) {
@@ -673,9 +690,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
         }
     }
     total = static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(total)));
-    const bool aligned = __reduce_max_sync(0xFFFFFFFFu, longest) <= kSplitAlign;
-    __syncthreads();
     const int ctas = min(static_cast<int>(gridDim.x), total);
+    const bool aligned = split_whole(__reduce_max_sync(0xFFFFFFFFu, longest), total / max(ctas, 1));
+    __syncthreads();
     if (static_cast<int>(blockIdx.x) >= ctas) {
         report(P.err, err);
         return;
@@ -1114,7 +1131,7 @@ __device__ __forceinline__ int prefill_pairs(const AttnParams &P, int r) {
     const int q0 = __ldg(P.a.q_start + r), q1 = __ldg(P.a.q_start + r + 1);
     if (!rows_valid(P.a, q0, q1)) return 0;
     const int64_t rows = static_cast<int64_t>(q1 - q0) * P.group;
-    return rows > kSplitMaxRows ? static_cast<int>((rows + 2 * kPrefillTile - 1) / (2 * kPrefillTile)) : 0;
+    return rows > P.split_rows ? static_cast<int>((rows + 2 * kPrefillTile - 1) / (2 * kPrefillTile)) : 0;
 }
 
 // The most keys that rows of a tile see, nearly: what its time goes with.
@@ -1814,6 +1831,7 @@ AttnParams attn_params(const df11_kv4_cache &c, const df11_kv4_attention_args &a
     P.err = err;
     P.wait_ns = 2000000000ull;
     P.parts = 1;
+    P.split_rows = static_cast<int64_t>(a.n_reqs) * c.n_heads <= kSplitFew ? kSplitRowsFew : kSplitRows;
     P.ws_parts = kMaxCtas;
     return P;
 }
@@ -1921,18 +1939,20 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
     Device dev;
     // rows, and the split path's places, are counted in 31 bits
     if (static_cast<int64_t>(a.n_tokens) * a.n_q_heads > INT32_MAX) return LaunchStatus::kUnsupported;
-    const int64_t tiles = (std::min<int64_t>(static_cast<int64_t>(a.max_q_len) * P.group, kSplitMaxRows) + kSplitCols - 1) / kSplitCols;
+    const int64_t tiles = (std::min<int64_t>(static_cast<int64_t>(a.max_q_len) * P.group, kSplitRowsFew) + kSplitCols - 1) / kSplitCols;
     const int64_t chunks =
         std::max<int64_t>(((static_cast<int64_t>(a.max_pages) << P.page_shift) + kSplitKeys - 1) / kSplitKeys, 1) + kSplitUnitCost;
     if (static_cast<double>(a.n_reqs) * P.kv_heads * tiles * chunks >= 2147483648.0) return LaunchStatus::kUnsupported;
     if (!prepare(&dev)) return LaunchStatus::kCuda;
     int64_t pairs = 0;
-    if (static_cast<int64_t>(a.max_q_len) * P.group > kSplitMaxRows) {
+    if (static_cast<int64_t>(a.max_q_len) * P.group > P.split_rows) {
         // as many pairs of tiles as the rows can make, the last one of each
-        // request that has more rows than the other path takes with one row
+        // request that has more rows than the other path takes with one row, and
+        // no request with more than max_q_len has
         const int64_t rows = static_cast<int64_t>(a.n_tokens) * P.group;
-        const int64_t some = std::min<int64_t>(a.n_reqs, rows / (kSplitMaxRows + 1));
-        pairs = (rows + some * (2 * kPrefillTile - 1)) / (2 * kPrefillTile);
+        const int64_t some = std::min<int64_t>(a.n_reqs, rows / (P.split_rows + 1));
+        const int64_t most = (static_cast<int64_t>(a.max_q_len) * P.group + 2 * kPrefillTile - 1) / (2 * kPrefillTile);
+        pairs = std::min((rows + some * (2 * kPrefillTile - 1)) / (2 * kPrefillTile), some * most);
         // where clusters of CTAs, one for each pair and head, run all at the same
         // time, they share the keys: 85 tokens in groups of 3 against 8192 keys of
         // 8 heads take 154 us alone (D = 64; 168 for D = 128), 31 (38) with 8

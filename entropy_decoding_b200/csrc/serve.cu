@@ -27,7 +27,9 @@ __device__ __forceinline__ void flag(int *err, uint32_t bits) {
 // them.  A row finds its request by bisection among the scanned starts; the
 // row that starts a page is the one that writes the page into the block table,
 // and every row computes its page's id from the free stack itself, so no
-// thread reads what another writes.
+// thread reads what another writes.  Bound by the launch and two rounds through
+// L2: 3.1 us for 128 requests of a token each, 4.9 us for 509 with up to 2048
+// new tokens each.
 constexpr int kExtendThreads = 512;
 
 __device__ __forceinline__ int64_t warp_incl(int64_t v, int lane) {
@@ -133,7 +135,10 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const df11_kv
 // A CTA takes a token, head_dim / 8 lanes a head, 8 elements (4 pairs) each.
 // The 64-bit angle and the sincos of a pair are paid once per token, while the
 // heads' loads are on their way.  The pass reads each element once and writes
-// it once; nothing else goes to memory.
+// it once; nothing else goes to memory.  8191 tokens of 32 + 8 heads of 128 in
+// BF16 take 40 us, 4.1 TB/s, bound by instructions (69 % of the issue slots; 35
+// us without norm and sine); 16 tokens 2.1 us.  A warp per token, which makes the
+// factors once, took 39 to 45 us for 2 to 5 heads in flight, and 2.3 for 16.
 constexpr int kRopeThreads = 128;
 constexpr int kRopeBatch = 5;  // heads whose loads a thread has in flight
 
@@ -289,9 +294,11 @@ LaunchStatus launch_kv_extend(const df11_kv_extend_args &a, int *err, cudaStream
 LaunchStatus launch_qk_norm_rope(const df11_qk_norm_rope_args &a, cudaStream_t s) {
     const int heads = a.q.n_heads + a.k.n_heads, per = kRopeThreads / (a.head_dim / 8);
     // few tokens: a CTA per token and group of heads, so that every element
-    // has its own thread at once; many: one CTA per token
+    // has its own thread at once; many: one CTA per token, which makes the
+    // angles once for all heads (32 + 8 heads of 128: 200 tokens 3.9 us in
+    // groups and 4.2 without, 300 tokens 4.8 and 4.3)
     const int groups = (heads + per - 1) / per;
-    const dim3 grid(a.n_tokens, static_cast<int64_t>(a.n_tokens) * groups <= 4 * 148 ? groups : 1);
+    const dim3 grid(a.n_tokens, static_cast<int64_t>(a.n_tokens) * groups <= 7 * 148 ? groups : 1);
     switch (a.head_dim) {
         case 64: launch_rope<64>(a, grid, s); break;
         case 128: launch_rope<128>(a, grid, s); break;
