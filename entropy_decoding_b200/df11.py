@@ -532,11 +532,35 @@ def df11_decode_gemm_launch_shape(mats, m: int):
 
 # ----------------------------------------------------------------- serving a block
 #
-# These run once per layer and token: pointers go to the library as they are (0 and None are NULL), with as little
-# Python in between as it takes.
+# These run once per layer and token: pointers go to the library as they are (0 and None are NULL), the arguments'
+# structures as bytes packed in one call, with as little Python in between as it takes.
 
-_kv_extend, _qk_norm_rope = _lib.df11_kv_extend, _lib.df11_qk_norm_rope
-_kv4_append, _kv4_gather, _kv4_attention = _lib.df11_kv4_append, _lib.df11_kv4_gather, _lib.df11_kv4_attention
+def _packer(cls):
+    """Packs the fields of a structure, those of structures inside it one after another, into its bytes."""
+    def layout(c):
+        fmt, at = "", 0
+        for name, t in c._fields_:
+            field = getattr(c, name)
+            inner, n = layout(t) if issubclass(t, ctypes.Structure) else (
+                {_P: "Q", _U64: "Q", ctypes.c_int32: "i", ctypes.c_float: "f"}[t], field.size)
+            fmt, at = fmt + "x" * (field.offset - at) + inner, field.offset + n
+        return fmt + "x" * (ctypes.sizeof(c) - at), ctypes.sizeof(c)
+
+    return struct.Struct("=" + layout(cls)[0]).pack
+
+
+def _packed(name, *before):
+    """The library's function with its argument structure as bytes."""
+    f = _lib[name]
+    f.argtypes, f.restype = [*before, ctypes.c_char_p, *_SIGS[name][0][len(before) + 1:]], _S
+    return f
+
+
+_extend_args, _rope_args, _attention_args = map(_packer, (KvExtendArgs, QkNormRopeArgs, Kv4AttentionArgs))
+_kv_extend, _qk_norm_rope = _packed("df11_kv_extend"), _packed("df11_qk_norm_rope")
+_kv4_attention = _packed("df11_kv4_attention", ctypes.POINTER(Kv4Cache))
+_kv4_append, _kv4_gather = _lib.df11_kv4_append, _lib.df11_kv4_gather
+_NO_SIDE = (0,) * len(RopeSide._fields_)
 
 
 def df11_kv_extend(kv_lens_ptr: int, new_lens_ptr: int, n_reqs: int, free_pages_ptr: int, n_free_ptr: int,
@@ -544,7 +568,7 @@ def df11_kv_extend(kv_lens_ptr: int, new_lens_ptr: int, n_reqs: int, free_pages_
                    slots_ptr: int, positions_ptr: int, max_tokens: int, n_free_out_ptr: int,
                    err_ptr: int | None = None, stream: int = 0):
     """One step's pages, block tables, slots and positions from the requests' lengths, all on the device."""
-    st = _kv_extend(KvExtendArgs(kv_lens_ptr, new_lens_ptr, n_reqs, max_pages, free_pages_ptr, n_free_ptr,
+    st = _kv_extend(_extend_args(kv_lens_ptr, new_lens_ptr, n_reqs, max_pages, free_pages_ptr, n_free_ptr,
                                  block_table_ptr, page_size, max_tokens, kv_lens_out_ptr, q_start_ptr, slots_ptr,
                                  positions_ptr, n_free_out_ptr), err_ptr, stream)
     if st:
@@ -555,8 +579,8 @@ def df11_qk_norm_rope(q, k, n_tokens: int, head_dim: int, positions_ptr: int, in
                       interleaved: bool = False, eps: float = 1e-6, dtype: str = "fp32", stream: int = 0):
     """q, k: (x pointer, token stride, norm weight pointer or 0, out pointer, out token stride, heads), strides in
     elements, or None: that side is absent.  dtype: of x, "fp32" or "bf16"; out is BF16."""
-    st = _qk_norm_rope(QkNormRopeArgs(q or (), k or (), n_tokens, head_dim, rot_dim, interleaved, ACTIVATIONS[dtype], eps,
-                                      positions_ptr, inv_freq_ptr), stream)
+    st = _qk_norm_rope(_rope_args(*(q or _NO_SIDE), *(k or _NO_SIDE), n_tokens, head_dim, rot_dim, interleaved,
+                                  ACTIVATIONS[dtype], eps, positions_ptr, inv_freq_ptr), stream)
     if st:
         raise Df11Error(st, "df11_qk_norm_rope")
 
@@ -593,9 +617,9 @@ def df11_kv4_attention(cache: Kv4Cache, q_ptr: int, q_token_stride: int, o_ptr: 
                        max_pages: int, n_tokens: int, max_q_len: int, scale: float, workspace_ptr: int,
                        workspace_bytes: int, causal: bool = True, window: int = 0, lse_ptr: int | None = None,
                        err_ptr: int | None = None, stream: int = 0):
-    st = _kv4_attention(cache, Kv4AttentionArgs(q_ptr, q_token_stride, o_ptr, o_token_stride, lse_ptr, q_start_ptr,
-                                                kv_lens_ptr, block_table_ptr, n_reqs, max_pages, n_tokens, n_q_heads,
-                                                max_q_len, causal, window, scale, workspace_ptr, workspace_bytes),
+    st = _kv4_attention(cache, _attention_args(q_ptr, q_token_stride, o_ptr, o_token_stride, lse_ptr or 0, q_start_ptr,
+                                               kv_lens_ptr, block_table_ptr or 0, n_reqs, max_pages, n_tokens, n_q_heads,
+                                               max_q_len, causal, window, scale, workspace_ptr, workspace_bytes),
                         err_ptr, stream)
     if st:
         raise Df11Error(st, "df11_kv4_attention")

@@ -54,6 +54,24 @@ def test_structures_and_constants_match_the_header(df11, tmp_path):
         assert view["const", c][0] == getattr(df11, py)
 
 
+def test_packed_arguments_are_the_structures(df11):
+    """The bytes that the calls pass are those of the structure with the same fields."""
+    def numbers(cls, i=3):
+        out = []
+        for _, t in cls._fields_:
+            out += numbers(t, i + 7) if issubclass(t, ctypes.Structure) else [0.5 * i if t is ctypes.c_float else i << 20]
+            i += 1
+        return out
+
+    def build(cls, values):
+        return cls(*[build(t, values) if issubclass(t, ctypes.Structure) else values.pop(0) for _, t in cls._fields_])
+
+    for cls, pack in ((df11.KvExtendArgs, df11._extend_args), (df11.QkNormRopeArgs, df11._rope_args),
+                      (df11.Kv4AttentionArgs, df11._attention_args)):
+        values = numbers(cls)
+        assert pack(*values) == bytes(build(cls, list(values)))
+
+
 def refused(df11, status, fn, *args, **kw):
     with pytest.raises(df11.Df11Error) as e:
         fn(*args, **kw)
