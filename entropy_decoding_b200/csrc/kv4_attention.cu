@@ -1951,7 +1951,7 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
         // no request with more than max_q_len has
         const int64_t rows = static_cast<int64_t>(a.n_tokens) * P.group;
         const int64_t some = std::min<int64_t>(a.n_reqs, rows / (P.split_rows + 1));
-        const int64_t most = (static_cast<int64_t>(a.max_q_len) * P.group + 2 * kPrefillTile - 1) / (2 * kPrefillTile);
+        const int64_t most = (std::min<int64_t>(a.max_q_len, a.n_tokens) * P.group + 2 * kPrefillTile - 1) / (2 * kPrefillTile);
         pairs = std::min((rows + some * (2 * kPrefillTile - 1)) / (2 * kPrefillTile), some * most);
         // where clusters of CTAs, one for each pair and head, run all at the same
         // time, they share the keys: 85 tokens in groups of 3 against 8192 keys of

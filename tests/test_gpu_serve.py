@@ -183,6 +183,13 @@ def test_rope(df11, t, hq, hk, d, rot, norm, far, dtype, inter):
     rope_case(df11, t, hq, hk, d, rot, dtype, norm, inter, far)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("t,hq,hk,d", [(1100, 100, 7, 128), (300, 100, 7, 64), (1, 300, 90, 256), (530, 45, 30, 256)])
+def test_rope_many_heads(df11, t, hq, hk, d, dtype):
+    """More heads than a thread has in flight."""
+    rope_case(df11, t, hq, hk, d, d, dtype, True, False, 5000)
+
+
 def test_rope_in_place(df11):
     rope_case(df11, 65, 6, 2, 128, 128, "bf16", True, False, 4000, in_place=True)
     rope_case(df11, 65, 6, 2, 64, 32, "bf16", True, True, 4000, in_place=True)
@@ -228,7 +235,7 @@ def some_kv(g, t, h, d, spread=1.0):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-@pytest.mark.parametrize("t,h,d,page,gk,gv", [(1, 1, 64, 16, 1.0, 1.0), (3, 2, 128, 16, 0.5, 2.0 ** -7), (65, 8, 128, 32, 1.0, 0.013),
+@pytest.mark.parametrize("t,h,d,page,gk,gv", [(1, 1, 64, 16, 1.0, 1.0), (3, 2, 128, 16, 0.5, 2.0 ** -7), (9, 40, 64, 16, 1.0, 0.5), (65, 8, 128, 32, 1.0, 0.013),
                                               (130, 5, 64, 128, 0.37, 1.9), (258, 3, 128, 64, 2.0 ** -12, 64.0)])
 def test_append_and_gather(df11, t, h, d, page, gk, gv, dtype):
     g = np.random.default_rng(t + d)
@@ -686,6 +693,37 @@ def test_graph_replays_with_other_lengths(df11):
                                                p.v[1500 * r:1500 * r + n], True, 0, 128 ** -0.5)
             bo, _ = ref.attention_bounds(wo, wl, wm, sm, vm, n, 128)
             assert ((got[0][r:r + 1].double().cpu().reshape(1, 8, 128) - wo).abs() <= bo).all()
+
+
+@pytest.mark.parametrize("hq,h,d", [(128, 1, 64), (300, 1, 128), (130, 130, 64)])
+def test_wide_groups_and_many_heads(df11, hq, h, d):
+    """A single token's rows of one cache head past those of the few-row kernel, and more cache heads than SMs."""
+    p = Problem(df11, [(1, 700), (1, 1), (2, 90), (1, 0)] if h == 1 else [(1, 90), (3, 40)], hq, h, d, 16, seed=hq)
+    for window in (0, 33):
+        o, lse, err = p.run(window=window)
+        assert err.item() == 0
+        p.check(o, lse, window=window)
+
+
+@pytest.mark.parametrize("n", [2, 140])
+def test_widest_bounds(df11, n):
+    """The largest window and the largest bound on a request's rows change nothing."""
+    p = Problem(df11, [(n, 500), (n, n), (n, 1)], 4, 2, 64, 16)
+    o, lse, _ = p.run()
+    for kw in (dict(window=2 ** 31 - 1), dict(max_q=2 ** 31 - 1)):
+        o2, lse2, err = p.run(**kw)
+        assert err.item() == 0
+        p.check(o2, lse2)
+
+
+@pytest.mark.parametrize("n", [2, 140])
+def test_rows_before_the_first_request(df11, n):
+    """Row starts that begin past row 0: the rows before are left as they were."""
+    p = Problem(df11, [(n, 500), (n, 300)], 4, 2, 64, 16, tail=5)
+    p.starts = p.starts + 3
+    o, lse, err = p.run()
+    assert err.item() == 0 and (o[:3] == 7.0).all() and (lse[:3] == 7.0).all()
+    p.check(o, lse)
 
 
 def test_graph_replays_a_mixed_batch(df11):
