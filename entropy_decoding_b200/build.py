@@ -32,7 +32,7 @@ SOURCES_CU = ["decode.cu", "encode.cu", "rans_decode.cu", "gemm.cu", "serve.cu",
               "kv4_attention.cu"]
 SOURCES_CPP = ["codec.cpp", "capi.cpp", "rans.cpp"]
 HEADERS = ["df11_internal.h", "codec.h", "launch.h", "encode.h", "rans.h", "walk.cuh", "gemm.h", "merge.cuh", "check.cuh",
-           "serve.h", "kv4.cuh", "tcgen05.cuh"]
+           "serve.h", "kv4.cuh", "tcgen05.cuh", "packed.cuh"]
 
 
 def _newer(target: str, deps: list[str]) -> bool:

@@ -7,6 +7,7 @@
 
 #include "df11.h"
 #include "kv4.cuh"
+#include "packed.cuh"
 #include "serve.h"
 
 namespace df11 {
@@ -17,8 +18,10 @@ namespace {
 // Neighbouring threads take the 4 tokens (whose 8-byte pieces of V codes and
 // bytes of V scales are neighbours where the tokens are), then the blocks of a
 // row, which are contiguous in the rows and, within a head, in the K codes.
-// 16,384 tokens of 8 heads of 128: append 21 us (86 MB, 4.1 TB/s), bound by
-// instructions (68 % of the issue slots, the quotients); gather 15 us, 5.7 TB/s.
+// 16,384 tokens of 8 heads of 128 (86 MB each way): append 17 us, 5.0 TB/s, bound
+// by latency and instructions (57 % of the issue slots, the quotients most of
+// them); gather 15 us, 5.7 TB/s.  CTAs of 128 threads take 0.7 us less of the 32,
+// and a step of 64 tokens 5.6 us, not 4.4.
 constexpr int kKv4Threads = 256;
 constexpr int kKv4Tokens = 4;
 
@@ -32,6 +35,7 @@ struct Kv4Params {
     int32_t n_tokens;
     int *err;
     const void *k, *v;  // append: the rows written
+    float k_inv, v_inv;  // of the scales, correctly rounded; 0: far from 1
     uint64_t k_stride, v_stride;
     void *k_out, *v_out;  // gather
 };
@@ -120,16 +124,25 @@ __device__ __forceinline__ float quotient(float x, float d, float r) {
     return fmaf(fmaf(-q, d, x), r, q);
 }
 
+__device__ __forceinline__ uint64_t quotient2(uint64_t x, float d, float r) {
+    const uint64_t r2 = pair(r, r), q = mul2(x, r2);
+    return fma2(fma2(q, pair(-d, -d), x), r2, q);
+}
+
 // The scale and the codes follow the definition step by step with correctly
 // rounded quotients: a block's scale has 4 significant bits and an element 8,
 // so quotients fall exactly on the borders between levels often, and a
-// reciprocal's last bit would move them.  A division per element took 34 us
-// for 16,384 tokens of 8 heads of 128; read and write are bound by memory so.
-__device__ __forceinline__ void quantize(const float (&x)[16], float g, uint2 &codes, uint32_t &scale) {
-    float top = 0.0f;  // fmaxf leaves NaN out
+// reciprocal's last bit would move them.  rg is 1 / g correctly rounded, or 0
+// where g is far from 1.  16,384 tokens of 8 heads of 128 took 34 us with a
+// division for each quotient, 21 with divisions for the scale's two.
+__device__ __forceinline__ void quantize(const float (&x)[16], float g, float rg, uint2 &codes, uint32_t &scale) {
+    float top = 0.0f;  // NaN left out
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
-    scale = f32_to_e4m3(fminf(__fdiv_rn(__fdiv_rn(top, 6.0f), g), 448.0f));
+    for (int i = 0; i < 16; i += 2) top = max3(top, fabsf(x[i]), fabsf(x[i + 1]));
+    const float wanted = rg > 0.0f && top > 0x1p-60f && top < 0x1p60f
+                             ? quotient(quotient(top, 6.0f, 1.0f / 6.0f), g, rg)
+                             : __fdiv_rn(__fdiv_rn(top, 6.0f), g);
+    scale = f32_to_e4m3(fminf(wanted, 448.0f));
     const uint32_t sh = e4m3x2_to_f16x2(scale);
     float s;
     asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(s) : "r"(sh));
@@ -138,10 +151,19 @@ __device__ __forceinline__ void quantize(const float (&x)[16], float g, uint2 &c
     if (!(step > 0.0f)) return;
     float y[2][8];
     if (step > 0x1p-100f && step < 0x1p100f) {
-        // what saturates anyway is brought to 8 steps first; a NaN goes with the positive ones
         const float r = __frcp_rn(step), most = 8.0f * step;
+        if (top <= most) {
+            // (a NaN beside them stays one, and its code is that of +6)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i / 8][i % 8] = quotient(fmaxf(fminf(x[i], most), -most), step, r);
+            for (int i = 0; i < 16; i += 2) {
+                const uint64_t q = quotient2(pair(x[i], x[i + 1]), step, r);
+                y[i / 8][i % 8] = low(q), y[i / 8][i % 8 + 1] = high(q);
+            }
+        } else {
+            // what saturates anyway is brought to 8 steps first; a NaN goes with the positive ones
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i / 8][i % 8] = quotient(fmaxf(fminf(x[i], most), -most), step, r);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i / 8][i % 8] = __fdiv_rn(x[i], step);
@@ -156,18 +178,20 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Params
     for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
         const int64_t t = static_cast<int64_t>(blockIdx.x) * kKv4Tokens + u % kKv4Tokens;
         const uint32_t hb = u / kKv4Tokens;  // block of the row
-        uint64_t slot;
-        if (!slot_of(P, t, slot)) continue;
+        if (t >= P.n_tokens) continue;
+        // the row is on its way while its slot is read, for nothing if it has none
         Sixteen<FP32> rk, rv;
         rk.load(P.k, t * P.k_stride + hb * kKv4Group);
         rv.load(P.v, t * P.v_stride + hb * kKv4Group);
+        uint64_t slot;
+        if (!slot_of(P, t, slot)) continue;
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v) {
             float x[16];
             (is_v ? rv : rk).get(x);
             uint2 codes;
             uint32_t scale;
-            quantize(x, is_v ? P.v_scale : P.k_scale, codes, scale);
+            quantize(x, is_v ? P.v_scale : P.k_scale, is_v ? P.v_inv : P.k_inv, codes, scale);
             uint8_t *cp, *sp;
             place<D>(P, is_v, slot, hb / NB, hb % NB, &cp, &sp);
             *reinterpret_cast<uint2 *>(cp) = codes;
@@ -260,6 +284,9 @@ unsigned threads_of(const df11_kv4_cache &c) {
     return units < kKv4Threads ? (units + 31) / 32 * 32 : kKv4Threads;
 }
 
+// 1 / g where the quotients by it need no special cases, else 0.
+float inverse(float g) { return g > 0x1p-60f && g < 0x1p60f ? 1.0f / g : 0.0f; }
+
 }  // namespace
 
 LaunchStatus launch_kv4_append(const df11_kv4_cache &c, const void *k, uint64_t k_stride, const void *v,
@@ -267,6 +294,8 @@ LaunchStatus launch_kv4_append(const df11_kv4_cache &c, const void *k, uint64_t 
                                cudaStream_t s) {
     Kv4Params P = params(c, slots, n_tokens, err);
     P.k = k;
+    P.k_inv = inverse(c.k_scale);
+    P.v_inv = inverse(c.v_scale);
     P.v = v;
     P.k_stride = k_stride;
     P.v_stride = v_stride;
