@@ -30,7 +30,7 @@ struct AttnParams {
     int32_t split_rows; // a request's rows that the few-row kernel takes at most
     int32_t parts;      // CTAs that share the keys of a pair of tiles (many rows)
     bool early;         // the many-row kernel may start before the few-row one has ended
-    uint32_t ws_parts;  // workspace, in floats: counters before, partial results from here
+    uint32_t ws_parts, ws_warps;  // workspace, in floats: counters, then the CTAs' partial results, then the warps'
 };
 
 // ------------------------------------------------------------------ few rows: keys shared out over the GPU
@@ -45,9 +45,9 @@ struct AttnParams {
 // want the decoded tile written to shared memory with 128 rows of which 8
 // columns are used; here nothing decoded is ever stored.
 // 64 requests of 256 to 16384 keys (8 cache heads of 128, groups of 4, 651 MB)
-// take 156 us, 4.2 TB/s; two of 98301 to 131072 keys 64 us.  Bound by instructions
-// at 3 warps a scheduler (1245 for a chunk: 512 conversions, 512 products with
-// the scales, 64 MMAs); copies alone took 118 us.
+// take 148 us, 4.4 TB/s; two of 98301 to 131072 keys 64 us.  Bound by instructions
+// at 3 warps a scheduler (some 1200 for a chunk: 512 conversions, 512 products
+// with the scales, 64 MMAs); copies alone took 118 us.
 constexpr int kSplitWarps = 12;
 constexpr int kSplitThreads = 32 * kSplitWarps;
 constexpr int kSplitCols = 8;      // rows of a unit
@@ -62,9 +62,9 @@ constexpr int kSplitRows = 32, kSplitRowsFew = 64;
 constexpr int kSplitFew = 16;  // requests times cache heads, at most, with the second bound
 // What a unit costs a CTA beside its chunks (queries, joins), in chunks: shares
 // are equal in this measure, in which a unit starts with so many empty places.
-// 64 requests of 256 to 16384 keys (8 cache heads of 128, groups of 4) take 182 us
-// with 0, 167 with 6, 160 with 10, 155 with 16 and 156 with 20; 2 of 98301 to
-// 131072 keys 67, 67, 65, 65 and 64.
+// With 4, 8 and 16, 64 requests of 256 to 16384 keys (8 cache heads of 128,
+// groups of 4) take 146, 146 and 148 us, 2 of 98301 to 131072 keys 66, 64 and 64,
+// one of 12000 18, 16 and 16, and 8 of 1000 16, 15 and 14.
 constexpr int kSplitUnitCost = 16;
 constexpr int32_t kMaxKeys = INT32_MAX - 255;
 
@@ -162,24 +162,20 @@ __device__ __forceinline__ SplitSeen split_seen(const AttnParams &P, const Split
     return s;
 }
 
-// Where a warp leaves its result of a unit for others: O (8 x kSplitPitch
-// floats, which spreads a thread's columns over the banks), then m and l.
-template <int D>
-constexpr int kSplitPitch = D + 4;
-
 template <int D>
 struct SplitShared {
     static constexpr uint32_t kStage = kSplitKeys * D * 9 / 8;  // a chunk's K and V
-    static constexpr uint32_t kResult = 4 * (kSplitCols * kSplitPitch<D> + 2 * kSplitCols);
-    static_assert(kResult <= kStage, "a result fits the stage of a chunk");
     alignas(128) uint8_t ring[kSplitWarps][kSplitStages][kStage];
     alignas(8) uint64_t full[kSplitWarps][kSplitStages];
     SplitPos pos[kSplitWarps][kSplitStages];  // of the chunk in a stage
     SplitSeen seen[kSplitWarps];
-    int ready[kSplitWarps];  // 2 x the segment (its end in the share) whose result is in a stage, + the stage
-    int freed[kSplitWarps];  // the last one that was taken from there
-    SplitPos last_pos, join_pos[2];
+    // A warp's results that others join: of the unit that its range starts
+    // inside, if that ends in the range (0, in the workspace), and of the one
+    // at its range's end (1, in shared memory); by the unit's first chunk, -1: none.
+    int part_unit[kSplitWarps][2];
+    SplitPos part_pos[kSplitWarps][2];
     int join_first[2], join_last[2], join[2];
+    SplitPos join_pos[2];
     int dead;  // a wait gave up: what the CTA has is not joined
 };
 
@@ -534,20 +530,21 @@ struct SplitShares {
     }
 };
 
-// A place in the launch: its request, the unit there, the offset in it, and the
-// places and the chunks before it.
+// A place in the launch: its request and the unit there, the unit's chunks, the
+// place's offset in it, and the chunks before the place.
 struct SplitPlace {
-    int r, unit, off, chunks;  // chunks: of each of the request's units
-    int at, before;            // the place itself; chunks of units before it, and its own unit's before it
+    int at, r, unit, chunks, off, before;
 };
 
-// Both ends of a share at once, by all lanes of a warp.
-__device__ __forceinline__ void split_find(const AttnParams &P, int lane, SplitPlace (&p)[2]) {
+// Finds N places, the last the greatest, with all lanes of a warp; a unit has
+// COST empty places before those of its chunks.
+template <int N, int COST>
+__device__ __forceinline__ void split_find(const AttnParams &P, int lane, SplitPlace (&p)[N]) {
     int base = 0, units = 0;
-    for (int b = 0; b < P.a.n_reqs && base <= p[1].at; b += 32) {
+    for (int b = 0; b < P.a.n_reqs && base <= p[N - 1].at; b += 32) {
         SplitReq q{};
         if (b + lane < P.a.n_reqs) q = split_req(P, b + lane);
-        const int w = q.units * (q.chunks + kSplitUnitCost);
+        const int size = q.chunks + COST, w = q.units * size;
         int incl = w, uncl = q.units;
 #pragma unroll
         for (int y = 1; y < 32; y <<= 1) {
@@ -556,44 +553,25 @@ __device__ __forceinline__ void split_find(const AttnParams &P, int lane, SplitP
         }
         const int at = base + incl - w, before = units + uncl - q.units;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < N; ++i) {
             const uint32_t holds = __ballot_sync(0xFFFFFFFFu, w && at <= p[i].at && p[i].at < at + w);
             if (!holds) continue;
-            const int src = __ffs(holds) - 1, size = q.chunks + kSplitUnitCost, in = p[i].at - at;
-            const int unit = size > 0 ? in / size : 0;
+            const int src = __ffs(holds) - 1, in = p[i].at - at, unit = size > 0 ? in / size : 0;
             p[i].r = b + src;
             p[i].unit = __shfl_sync(0xFFFFFFFFu, unit, src);
             p[i].off = __shfl_sync(0xFFFFFFFFu, in - unit * size, src);
             p[i].chunks = __shfl_sync(0xFFFFFFFFu, q.chunks, src);
-            // empty places before it: those of the units before, and its own unit's
-            p[i].before = p[i].at - (__shfl_sync(0xFFFFFFFFu, before + unit, src)) * kSplitUnitCost - min(p[i].off, kSplitUnitCost);
+            p[i].before = p[i].at - __shfl_sync(0xFFFFFFFFu, before + unit, src) * COST - min(p[i].off, COST);
         }
         base += __shfl_sync(0xFFFFFFFFu, incl, 31);
         units += __shfl_sync(0xFFFFFFFFu, uncl, 31);
     }
-    if (base <= p[1].at) {  // the end of the launch
-        p[1].off = 0;
-        p[1].before = base - units * kSplitUnitCost;
-    }
-}
-
-// Waits until every lane's flag word (null: none), but for the bits `loose`,
-// holds `want`; false after limit_ns, which sets *dead, or when *dead is set.
-__device__ __forceinline__ bool flags_wait(const int *flag, int want, int loose, int *dead, uint64_t limit_ns) {
-    auto there = [&]() {
-        return __all_sync(0xFFFFFFFFu, !flag || (*reinterpret_cast<const volatile int *>(flag) & ~loose) == want) != 0;
-    };
-    bool ok = there();
-    if (!ok) {
-        const uint64_t t0 = global_ns();
-        while (!(ok = there())) {
-            const bool late = global_ns() - t0 > limit_ns;
-            if (late) atomicExch(dead, 1);
-            if (__any_sync(0xFFFFFFFFu, late || *reinterpret_cast<volatile int *>(dead))) break;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (base <= p[i].at) {  // the end of the launch
+            p[i].off = 0;
+            p[i].before = base - units * COST;
         }
-    }
-    __threadfence_block();
-    return ok;
 }
 
 // A thread's part of a warp's result: columns 2t and 2t + 1, elements [g D / 8, (g + 1) D / 8).
@@ -602,41 +580,63 @@ __device__ __forceinline__ void split_put(float *at, int lane, const SplitUnit<D
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        float *o = at + (2 * t + c) * kSplitPitch<D> + g * (D / 8);
+        float *o = at + (2 * t + c) * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2)
             *reinterpret_cast<float4 *>(o + 2 * i) = make_float4(U.o[i][c], U.o[i][2 + c], U.o[i + 1][c], U.o[i + 1][2 + c]);
         if (g == 0) {
-            at[kSplitCols * kSplitPitch<D> + 2 * t + c] = U.m[c];
-            at[kSplitCols * kSplitPitch<D> + kSplitCols + 2 * t + c] = U.l[c];
+            at[kSplitCols * D + 2 * t + c] = U.m[c];
+            at[kSplitCols * D + kSplitCols + 2 * t + c] = U.l[c];
         }
     }
 }
 
+// Column col, elements [d, d + 4) of partial results joined one after another.
+template <int D>
+struct SplitJoin {
+    float m = -INFINITY, l = 0.0f, o[4] = {};
+    template <int N>
+    __device__ __forceinline__ void add(const float (&mb)[N], const float (&lb)[N], const float4 (&ob)[N]) {
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = fmaxf(top, mb[i]);
+        const float sh = top == -INFINITY ? 0.0f : top, f = ex2(m - sh);
+        m = top;
+        l *= f, o[0] *= f, o[1] *= f, o[2] *= f, o[3] *= f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float h = ex2(mb[i] - sh);
+            l += lb[i] * h;
+            o[0] += ob[i].x * h, o[1] += ob[i].y * h, o[2] += ob[i].z * h, o[3] += ob[i].w * h;
+        }
+    }
+};
+
 // Whether units of at most `longest` chunks are not divided between CTAs, whose
-// shares are of `share` places: units of a chunk a warp, and those that come
-// to about one or two a CTA.  A join of CTAs takes 1 to 3 us, and the last CTA to
-// finish has up to a unit more.  8 heads of 128: one token on 500 keys 10.1 us
-// whole, 11.2 divided; on 1000 12.9 and 11.5; 8 tokens on 1000 keys each 13.4
-// and 15.4, on 3000 20.6 and 19.0; 32 on 2000 28.8 and 31.5; 100 on 2000 82.6
-// and 80.4.
+// shares are of `share` places: units of a chunk a warp, and those that come to
+// one or a few a CTA.  A join of CTAs takes 1 to 3 us, and the last CTA to finish
+// has up to a unit more.  8 heads of 128, whole and divided: one token on 500
+// keys 11.1 and 11.8 us, on 2000 15.9 and 12.5; 8 tokens on 1000 keys each 13.5
+// and 15.3, on 3000 20.5 and 18.8; 32 on 2000 27.4 and 30.3; 100 on 1000 43.9 and
+// 48.5, on 2000 66.7 and 69.0, on 3000 92.4 and 89.7; 8 with 24 rows each on
+// 8000 keys 74 and 58.
 __device__ __forceinline__ bool split_whole(int longest, int share) {
-    return longest <= kSplitWarps || (longest <= share + share / 4 && share <= 128);
+    return longest <= kSplitWarps || (longest <= 4 * kSplitWarps && longest <= share + share / 4 && share <= 320);
 }
 
 // Persistent CTAs, each a contiguous, equal share of the launch's chunks
 // (request, unit, chunk in order), so a long request spreads over the GPU and
-// short ones share a CTA, whatever the mix.  A share's chunks go to the warps
-// in turn, and the warps run on their own, each with a ring of two chunks that
-// its own copies fill, across unit ends.  A unit's part in a share is a
-// segment.  Within the share, a warp leaves its result of a segment in the
-// stage it has just used and goes on; the warp with the segment's last chunk
-// joins them.  The share's last segment is joined by the whole CTA.  A unit
-// that spans CTAs goes through the workspace, and the CTA that arrives last
-// joins its parts at its own end, in order: no CTA waits for another, and the
-// result does not depend on which one was last.  Where units are short
-// (split_whole), a unit goes whole to the CTA whose share holds its first
-// chunk: fewer CTAs work, but none joins.
+// short ones share a CTA, whatever the mix; each warp a contiguous part of its
+// CTA's share.  The warps run on their own, each with a ring of two chunks that
+// its own copies fill, across unit ends.  (With a chunk to each warp in turn,
+// every unit was joined from 12 results: 156 us instead of 148, and 100 requests
+// of 500 keys 35 instead of 29.)  A unit that lies in a warp's range is
+// finished there; of others the warp leaves its part, and the CTA joins the
+// parts of each unit at the end.  A unit that spans CTAs goes through the
+// workspace, and the CTA that arrives last joins its parts, in order: no warp or
+// CTA waits for another, and the result does not depend on which one was last.
+// Where units are short (split_whole), a unit goes whole to the CTA whose
+// share holds its first chunk: fewer CTAs work, but none joins.
 template <int D, int ES>
 __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -649,12 +649,12 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
 #pragma unroll
         for (int i = 0; i < kSplitStages; ++i) mbar_init(&S.full[warp][i], 1);
         fence_mbar_init();
-        S.ready[warp] = S.freed[warp] = -1;
+        S.part_unit[warp][0] = S.part_unit[warp][1] = -1;
         if (warp < 2) S.join[warp] = 0;
         if (warp == 0) S.dead = 0;
     }
 
-    // ---- the launch's chunks (the host has seen that they fit 31 bits);
+    // ---- the launch's places (the host has seen that they fit 31 bits);
     // every warp counts them by itself, so none waits
     int total = 0, longest = 0;
     for (int r = lane; r < A.n_reqs; r += 32) {
@@ -674,13 +674,13 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
         report(P.err, err);
         return;
     }
-    // ---- the share: no share of places is empty, and a unit's chunks follow one
+    // ---- the CTA's share: no share of places is empty, and a unit's chunks follow one
     // another, so its parts are those of every CTA from its first chunk's to its last's
     const SplitShares shares{total / ctas, total % ctas};
     SplitPlace ends[2];
     ends[0].at = shares.start(blockIdx.x);
     ends[1].at = shares.start(blockIdx.x + 1);
-    split_find(P, lane, ends);
+    split_find<2, kSplitUnitCost>(P, lane, ends);
     // first places of the units that the ends lie in
     const int unit0 = ends[0].at - ends[0].off, unit1 = ends[1].at - ends[1].off;
     if (aligned) {
@@ -689,36 +689,41 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
         for (int i = 0; i < 2; ++i)
             if (ends[i].off) ends[i].before += ends[i].chunks - max(ends[i].off - kSplitUnitCost, 0);
     }
-    const int share = ends[1].before - ends[0].before;  // chunks; indexes from here on count from the first of them
-    if (share <= 0) {
+    // chunks [x0, x1) of the launch, and this warp's of them
+    const int x0 = ends[0].before, x1 = ends[1].before, per = (x1 - x0) / kSplitWarps, more = (x1 - x0) % kSplitWarps;
+    if (x0 >= x1) {
         report(P.err, err);
         return;
     }
-    SplitPos ahead;  // of this warp's next chunk to copy
-    ahead.r = ends[0].r;
-    ahead.q = split_req(P, ahead.r);
-    ahead.head = ends[0].unit / ahead.q.tiles;
-    ahead.tile = ends[0].unit % ahead.q.tiles;
-    ahead.c = max(ends[0].off - kSplitUnitCost, 0);
-    if (aligned && ends[0].off) ahead.advance(P, ahead.q.chunks - ahead.c);
+    const int w0 = x0 + warp * per + min(warp, more), share = per + (warp < more);
 
     // ---- this warp's copies, up to two chunks ahead of its computation
-    int ax = 0;         // index of `ahead`
-    bool next = false;  // there is a chunk at `ahead` for this warp
+    SplitPos ahead;  // of its next chunk to copy
+    if (share) {
+        // in the share's first request, if it has so many chunks, else looked for
+        ahead.r = ends[0].r;
+        ahead.q = split_req(P, ahead.r);
+        const int skip = aligned && ends[0].off ? ahead.q.chunks : max(ends[0].off - kSplitUnitCost, 0);
+        int at = ends[0].unit * ahead.q.chunks + skip + (w0 - x0);
+        if (at >= ahead.q.units * ahead.q.chunks) {
+            SplitPlace start[1];
+            start[0].at = w0;
+            split_find<1, 0>(P, lane, start);
+            ahead.r = start[0].r;
+            ahead.q = split_req(P, ahead.r);
+            at = start[0].unit * ahead.q.chunks + start[0].off;
+        }
+        const int unit = at / ahead.q.chunks;
+        ahead.head = unit / ahead.q.tiles;
+        ahead.tile = unit % ahead.q.tiles;
+        ahead.c = at - unit * ahead.q.chunks;
+    }
+    int copied = 0;
     uint32_t pages[kSplitStages] = {};
     int64_t id = kNoPage;
-    auto seek = [&](int by) {
-        ax += by;
-        next = ax < share;
-        if (next) {
-            ahead.advance(P, by);
-            id = split_page<ES>(P, ahead, lane);
-        }
-    };
+    if (share) id = split_page<ES>(P, ahead, lane);
     // copies the chunk at `ahead` into stage st and moves on to the one after
-    int issued = 0, landed = 0;
     auto issue = [&](int st) {
-        ++issued;
         if (lane == 0) S.pos[warp][st] = ahead;
         const bool have = id >= 0 && static_cast<uint64_t>(id) < P.n_pages;
         if (!have && id != kNoPage) err |= DF11_DEV_ERR_PAGES;
@@ -728,29 +733,29 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
         split_issue<D, ES>(P, block, have, mask, (ahead.q.c_lo + ahead.c) & 1, lane, S.ring[warp][st], &S.full[warp][st]);
         if (st) pages[1] = mask;
         else pages[0] = mask;
-        seek(kSplitWarps);
+        if (++copied < share) {
+            ahead.advance(P, 1);
+            id = split_page<ES>(P, ahead, lane);
+        }
     };
-    seek(warp);
 #pragma unroll 1
-    for (int i = 0; i < kSplitStages && next; ++i) issue(i);
+    for (int i = 0; i < kSplitStages && i < share; ++i) issue(i);
 
+    const int g = lane >> 2, t = lane & 3;
     SplitUnit<D> U;
-    bool dead = false;   // a wait gave up: no more copies
-    int held = -1;       // the segment whose result is in the stage that the next copy goes to
-    bool in_last = false;  // U is this warp's part of the share's last segment
-    for (int cx = warp, st = 0, parity = 0, s0 = 0, s1 = 0; cx < share; cx += kSplitWarps) {
+    bool dead = false;  // a wait gave up: no more copies
+    for (int cx = 0, st = 0, parity = 0, s0 = 0; cx < share; ++cx) {
         const SplitPos &at = S.pos[warp][st];
         __syncwarp();
-        if (cx >= s1) {
-            s0 = max(cx - at.c, 0);
-            s1 = min(cx - at.c + at.q.chunks, share);
+        if (cx == 0 || at.c == 0) {
+            s0 = cx;
             if (lane == 0) S.seen[warp] = split_seen(P, at);
             split_load_unit<D>(P, at, lane, U);
             __syncwarp();
         }
         const int key0 = at.key0();
         const SplitSeen &seen = S.seen[warp];
-        uint8_t *stage = S.ring[warp][st];
+        const uint8_t *stage = S.ring[warp][st];
         uint32_t there = st ? pages[1] : pages[0];
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.full[warp][st], parity, P.wait_ns))) {
             err |= DF11_DEV_ERR_TIMEOUT;
@@ -759,7 +764,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
             if (lane == 0) atomicExch(&S.dead, 1);
             mbar_wait(&S.full[warp][st], parity, P.wait_ns);  // the memory is not given up with a copy on its way
         }
-        ++landed;
         const bool whole = there == (1u << (kSplitKeys >> ES)) - 1u && key0 >= seen.all_lo && key0 + kSplitKeys <= seen.all_hi;
         float s[4][4];
         split_scores<D, ES>(P, stage, key0, there, whole, seen, lane, U, s);
@@ -767,213 +771,160 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
         split_softmax<D>(s, U, pb);
         split_values<D, ES>(stage, key0, there, whole, seen, lane, U, pb);
         __syncwarp();
-        // the other stage, if a result was in it until now: taken by now, as a
-        // rule, and waited for before this warp leaves another
-        if (held >= 0 && !dead) {
-            if (!flags_wait(lane == 0 ? &S.freed[warp] : nullptr, held, 0, &S.dead, P.wait_ns)) {
-                err |= DF11_DEV_ERR_TIMEOUT;
-                dead = true;
-            } else if (next) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                issue(st ^ 1);
-            }
-        }
-        held = -1;
-        bool keep = false;  // the stage holds a result
-        if (cx + kSplitWarps >= s1) {
-            // ---- the end of the segment [s0, s1) for this warp
+        const bool ends_unit = at.c + 1 == at.q.chunks;
+        if (ends_unit || cx + 1 == share) {
+            // ---- the end of the unit, or of the range in it
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int y = 4; y < 32; y <<= 1) U.l[c] += __shfl_xor_sync(0xFFFFFFFFu, U.l[c], y);
-            if (s1 == share) {
-                in_last = true;
-                if (lane == 0 && cx == share - 1) S.last_pos = at;
-            } else if (cx != s1 - 1) {
-                split_put<D>(reinterpret_cast<float *>(stage), lane, U);
-                __threadfence_block();
-                __syncwarp();
-                if (lane == 0) *reinterpret_cast<volatile int *>(&S.ready[warp]) = 2 * s1 + st;
-                keep = true;
+            if (ends_unit && cx - s0 == at.c) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float o[D / 8];
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) o[2 * i] = U.o[i][c], o[2 * i + 1] = U.o[i][2 + c];
+                    split_store<D, D / 8>(P, at, 2 * t + c, g * (D / 8), o, U.m[c], U.l[c]);
+                }
             } else {
-                // join: this warp's result is in registers; lane i looks at the segment's i-th warp
-                const int warps = min(s1 - s0, kSplitWarps), g = lane >> 2, t = lane & 3;
-                const int mate = (s0 + lane) % kSplitWarps;
-                const bool other = lane < warps && mate != warp;
-                if (!flags_wait(other ? &S.ready[mate] : nullptr, 2 * s1, 1, &S.dead, P.wait_ns)) {
-                    err |= DF11_DEV_ERR_TIMEOUT;
-                    dead = true;
+                const int last = cx + 1 == share;
+                if (lane == 0) {
+                    S.part_unit[warp][last] = w0 + cx - at.c;
+                    S.part_pos[warp][last] = at;
                 }
-                for (int i = 0; i < warps; ++i) {
-                    const int w = (s0 + i) % kSplitWarps;
-                    if (w == warp) continue;
-                    const float *r = reinterpret_cast<const float *>(S.ring[w][S.ready[w] & 1]);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float mw = r[kSplitCols * kSplitPitch<D> + 2 * t + c], mn = fmaxf(U.m[c], mw);
-                        const float sh = mn == -INFINITY ? 0.0f : mn, f = ex2(U.m[c] - sh), h = ex2(mw - sh);
-                        U.m[c] = mn;
-                        U.l[c] = U.l[c] * f + h * r[kSplitCols * kSplitPitch<D> + kSplitCols + 2 * t + c];
-                        const float *o = r + (2 * t + c) * kSplitPitch<D> + g * (D / 8);
-#pragma unroll
-                        for (int y = 0; y < D / 16; y += 2) {
-                            const float4 v = *reinterpret_cast<const float4 *>(o + 2 * y);
-                            U.o[y][c] = U.o[y][c] * f + h * v.x, U.o[y][2 + c] = U.o[y][2 + c] * f + h * v.y;
-                            U.o[y + 1][c] = U.o[y + 1][c] * f + h * v.z, U.o[y + 1][2 + c] = U.o[y + 1][2 + c] * f + h * v.w;
-                        }
-                    }
-                }
-                __threadfence_block();
-                __syncwarp();
-                if (other) *reinterpret_cast<volatile int *>(&S.freed[mate]) = s1;
-                if (s1 - s0 == at.q.chunks) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float o[D / 8];
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) o[2 * i] = U.o[i][c], o[2 * i + 1] = U.o[i][2 + c];
-                        split_store<D, D / 8>(P, at, 2 * t + c, g * (D / 8), o, U.m[c], U.l[c]);
-                    }
-                } else {
-                    // the share starts inside this unit: its part, of those of CTAs first .. last (this one)
-                    const int first = shares.owner(unit0 + kSplitUnitCost), last = blockIdx.x;
-                    float *p = static_cast<float *>(A.workspace) + P.ws_parts +
-                               2ull * blockIdx.x * split_partial_floats<D>();
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                        for (int i = 0; i < D / 16; i += 2)
-                            __stcg(reinterpret_cast<float4 *>(p + (2 * t + c) * D + g * (D / 8) + 2 * i),
-                                   make_float4(U.o[i][c], U.o[i][2 + c], U.o[i + 1][c], U.o[i + 1][2 + c]));
-                        if (g == 0) {
-                            __stcg(p + kSplitCols * D + 2 * t + c, U.m[c]);
-                            __stcg(p + kSplitCols * D + kSplitCols + 2 * t + c, U.l[c]);
-                        }
-                    }
-                    __threadfence();
-                    __syncwarp();
-                    if (lane == 0) {
-                        int *counter = static_cast<int *>(A.workspace) + first;
-                        if (atomicAdd(counter, 1) == last - first) {
-                            *counter = 0;
-                            __threadfence();
-                            S.join_pos[0] = at;
-                            S.join_first[0] = first;
-                            S.join_last[0] = last;
-                            S.join[0] = 1;
-                        }
-                    }
-                }
+                if (!last)
+                    split_put<D>(static_cast<float *>(A.workspace) + P.ws_warps +
+                                     static_cast<uint64_t>(blockIdx.x * kSplitWarps + warp) * split_partial_floats<D>(),
+                                 lane, U);
             }
         }
-        if (keep) {
-            held = s1;
-        } else if (next && !dead) {
+        if (dead) {
+            // the rest of the range is given up, but for the copy that may still be out
+            if (copied > cx + 1) mbar_wait(&S.full[warp][st ^ 1], parity ^ st, P.wait_ns);
+            break;
+        }
+        if (copied < share) {
             fence_proxy_async_smem();
             issue(st);
-        }
-        if (dead) {
-            // the rest of the share is given up, but for the copy that may still be out
-            if (issued > landed) mbar_wait(&S.full[warp][st ^ 1], parity ^ st, P.wait_ns);
-            break;
         }
         st ^= 1;
         if (!st) parity ^= 1;
     }
 
-    // ---- the share's last segment, joined by the CTA
+    // ---- the units that warps have left parts of, a column to a warp at a time
     __syncthreads();
     if (S.dead) {
         report(P.err, __reduce_or_sync(0xFFFFFFFFu, err) * (lane == 0));
         return;
     }
     float *results = reinterpret_cast<float *>(&S.ring[0][0][0]);
-    constexpr int kResult = SplitShared<D>::kResult / 4;
-    const SplitPos last = S.last_pos;
-    const int n_last = min(last.c + 1, share), s0 = share - n_last;  // its chunks of the share: from s0 on
-    const int warps = min(n_last, kSplitWarps);
-    if (in_last) split_put<D>(results + warp * kResult, lane, U);
+    constexpr int kPart = split_partial_floats<D>();
+    static_assert(kPart * 4 <= static_cast<int>(SplitShared<D>::kStage * kSplitStages), "results fit the rings");
+    if (S.part_unit[warp][1] >= 0) split_put<D>(results + warp * kPart, lane, U);
     __syncthreads();
-    const bool whole_unit = n_last == last.q.chunks;
-    const int u0 = (s0 > 0 ? unit1 : unit0) + kSplitUnitCost;  // place of the unit's first chunk
-    const int first = whole_unit ? 0 : shares.owner(u0), final = whole_unit ? 0 : shares.owner(u0 + last.q.chunks - 1);
+    const float *early = static_cast<const float *>(A.workspace) + P.ws_warps +
+                         static_cast<uint64_t>(blockIdx.x) * kSplitWarps * kPart;
     // a CTA's parts: of the unit that its share starts inside (0), and of the one that goes on in the next CTA's (1)
-    auto part = [&](int cta, int first_cta) {
-        return static_cast<float *>(A.workspace) + P.ws_parts +
-               (2ull * cta + (cta == first_cta ? 1 : 0)) * split_partial_floats<D>();
+    auto cta_part = [&](int cta, int first) {
+        return static_cast<float *>(A.workspace) + P.ws_parts + (2ull * cta + (cta == first ? 1 : 0)) * kPart;
     };
-    for (int it = tid; it < kSplitCols * D / 4; it += kSplitThreads) {
-        const int col = it / (D / 4), d = it % (D / 4) * 4;
-        float m = -INFINITY, l = 0.0f, o[4] = {};
-        for (int i = 0; i < warps; ++i) m = fmaxf(m, results[(s0 + i) % kSplitWarps * kResult + kSplitCols * kSplitPitch<D> + col]);
-        const float sh = m == -INFINITY ? 0.0f : m;
+    // the warps whose part at the range's end is the first of its unit, and
+    // above them, if the first warp has one, its early part, which is alone
+    uint32_t units;
+    {
+        const int u = lane < kSplitWarps ? S.part_unit[lane][1] : -1, before = __shfl_up_sync(0xFFFFFFFFu, u, 1);
+        units = __ballot_sync(0xFFFFFFFFu, u >= 0 && (lane == 0 || before != u)) |
+                (S.part_unit[0][0] >= 0 ? 1u << kSplitWarps : 0u);
+    }
+    int task = 0;
+#pragma unroll 1
+    for (; units; units &= units - 1) {
+        const int cand = __ffs(units) - 1, which = cand < kSplitWarps, lead = which ? cand : 0;
+        const int unit = S.part_unit[lead][which];
+        const SplitPos &at = S.part_pos[lead][which];
+        const bool in_share = unit >= x0 && unit + at.q.chunks <= x1;
+        // of a unit that spans CTAs: the place of its first chunk, and the CTAs
+        const int u0 = (unit < x0 ? unit0 : unit1) + kSplitUnitCost;
+        const int first = in_share ? 0 : shares.owner(u0), last = in_share ? 0 : shares.owner(u0 + at.q.chunks - 1);
+        if (!in_share && tid == 0) {
+            const int kind = unit < x0 ? 0 : 1;
+            S.join[kind] = 1;
+            S.join_first[kind] = first;
+            S.join_last[kind] = last;
+            S.join_pos[kind] = at;
+        }
+        // its parts: `n` warps' at their ends, then perhaps an early one
+        int n = 0;
+        if (which)
+            while (lead + n < kSplitWarps && S.part_unit[lead + n][1] == unit) ++n;
+        const bool tail = lead + n < kSplitWarps && S.part_unit[lead + n][0] == unit;
+        const float *ends_at = results + lead * kPart, *tail_at = early + (lead + n) * kPart;
+        for (int col = 0; col < kSplitCols; ++col, ++task) {
+            if (task % kSplitWarps != warp || lane >= D / 4) continue;
+            const int d = 4 * lane;
+            float m = tail ? tail_at[kSplitCols * D + col] : -INFINITY, l = 0.0f, o[4] = {};
 #pragma unroll 4
-        for (int i = 0; i < warps; ++i) {
-            const float *r = results + (s0 + i) % kSplitWarps * kResult;
-            const float h = ex2(r[kSplitCols * kSplitPitch<D> + col] - sh);
-            const float4 v = *reinterpret_cast<const float4 *>(r + col * kSplitPitch<D> + d);
-            l += h * r[kSplitCols * kSplitPitch<D> + kSplitCols + col];
-            o[0] += h * v.x, o[1] += h * v.y, o[2] += h * v.z, o[3] += h * v.w;
-        }
-        if (whole_unit) {
-            split_store<D, 4>(P, last, col, d, o, m, l);
-        } else {
-            float *p = part(blockIdx.x, first);
-            __stcg(reinterpret_cast<float4 *>(p + col * D + d), make_float4(o[0], o[1], o[2], o[3]));
-            if (d == 0) {
-                __stcg(p + kSplitCols * D + col, m);
-                __stcg(p + kSplitCols * D + kSplitCols + col, l);
+            for (int i = 0; i < n; ++i) m = fmaxf(m, ends_at[i * kPart + kSplitCols * D + col]);
+            const float sh = m == -INFINITY ? 0.0f : m;
+            auto take = [&](const float *r) {
+                const float h = ex2(r[kSplitCols * D + col] - sh);
+                const float4 v = *reinterpret_cast<const float4 *>(r + col * D + d);
+                l += h * r[kSplitCols * D + kSplitCols + col];
+                o[0] += h * v.x, o[1] += h * v.y, o[2] += h * v.z, o[3] += h * v.w;
+            };
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) take(ends_at + i * kPart);
+            if (tail) take(tail_at);
+            if (in_share) {
+                split_store<D, 4>(P, at, col, d, o, m, l);
+            } else {
+                float *p = cta_part(blockIdx.x, first);
+                __stcg(reinterpret_cast<float4 *>(p + col * D + d), make_float4(o[0], o[1], o[2], o[3]));
+                if (lane == 0) {
+                    __stcg(p + kSplitCols * D + col, m);
+                    __stcg(p + kSplitCols * D + kSplitCols + col, l);
+                }
             }
         }
     }
-    if (!whole_unit) {
-        __syncthreads();
-        if (tid == 0) {
-            __threadfence();  // the CTA's stores, seen at the barrier, before the arrival
-            int *counter = static_cast<int *>(A.workspace) + first;
-            if (atomicAdd(counter, 1) == final - first) {
-                *counter = 0;
-                __threadfence();
-                S.join_pos[1] = last;
-                S.join_first[1] = first;
-                S.join_last[1] = final;
-                S.join[1] = 1;
-            }
-        }
-    }
-    // ---- units whose last part was this CTA's
+    // ---- units that span CTAs: joined by the CTA whose part is the last
     __syncthreads();
+    if (!S.join[0] && !S.join[1]) {
+        report(P.err, __reduce_or_sync(0xFFFFFFFFu, err) * (lane == 0));
+        return;
+    }
+    if (tid == 0) {
+        __threadfence();  // the CTA's stores, seen at the barrier, before the arrivals
+        for (int kind = 0; kind < 2; ++kind) {
+            if (!S.join[kind]) continue;
+            int *counter = static_cast<int *>(A.workspace) + S.join_first[kind];
+            S.join[kind] = atomicAdd(counter, 1) == S.join_last[kind] - S.join_first[kind];
+            if (S.join[kind]) *counter = 0;
+        }
+        __threadfence();
+    }
+    __syncthreads();
+#pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         if (!S.join[kind]) continue;
         const int b0 = S.join_first[kind], b1 = S.join_last[kind];
         for (int it = tid; it < kSplitCols * D / 4; it += kSplitThreads) {
             const int col = it / (D / 4), d = it % (D / 4) * 4;
-            float m = -INFINITY, l = 0.0f, o[4] = {};
+            SplitJoin<D> J;
+#pragma unroll 1
             for (int b = b0; b <= b1; b += 8) {
                 float mb[8], lb[8];
                 float4 ob[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float *p = part(min(b + i, b1), b0);
+                    const float *p = cta_part(min(b + i, b1), b0);
                     mb[i] = b + i > b1 ? -INFINITY : __ldcg(p + kSplitCols * D + col);
                     lb[i] = __ldcg(p + kSplitCols * D + kSplitCols + col);
                     ob[i] = __ldcg(reinterpret_cast<const float4 *>(p + col * D + d));
                 }
-                float top = m;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, mb[i]);
-                const float sh = top == -INFINITY ? 0.0f : top, f = ex2(m - sh);
-                m = top;
-                l *= f, o[0] *= f, o[1] *= f, o[2] *= f, o[3] *= f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float h = ex2(mb[i] - sh);
-                    l += lb[i] * h;
-                    o[0] += ob[i].x * h, o[1] += ob[i].y * h, o[2] += ob[i].z * h, o[3] += ob[i].w * h;
-                }
+                J.add(mb, lb, ob);
             }
-            split_store<D, 4>(P, S.join_pos[kind], col, d, o, m, l);
+            split_store<D, 4>(P, S.join_pos[kind], col, d, J.o, J.m, J.l);
         }
     }
     report(P.err, __reduce_or_sync(0xFFFFFFFFu, err) * (lane == 0));
@@ -1814,6 +1765,7 @@ AttnParams attn_params(const df11_kv4_cache &c, const df11_kv4_attention_args &a
     P.parts = 1;
     P.split_rows = static_cast<int64_t>(a.n_reqs) * c.n_heads <= kSplitFew ? kSplitRowsFew : kSplitRows;
     P.ws_parts = kMaxCtas;
+    P.ws_warps = kMaxCtas + 2 * kMaxCtas * (c.head_dim == 128 ? split_partial_floats<128>() : split_partial_floats<64>());
     return P;
 }
 
@@ -1910,7 +1862,7 @@ bool prepare(Device *d) {
 
 LaunchStatus kv4_attention_workspace(const df11_kv4_cache &c, const df11_kv4_attention_args &, uint64_t *bytes) {
     const uint64_t part = c.head_dim == 128 ? split_partial_floats<128>() : split_partial_floats<64>();
-    *bytes = 4 * (kMaxCtas + 2 * kMaxCtas * part);
+    *bytes = 4 * (kMaxCtas + (2 + kSplitWarps) * kMaxCtas * part);
     return LaunchStatus::kOk;
 }
 

@@ -497,8 +497,8 @@ def test_many_requests(df11, n):
 
 @pytest.mark.parametrize("hq,h,d,page", [(8, 8, 64, 16), (8, 4, 128, 64), (4, 4, 64, 128)])
 def test_long_batches(df11, hq, h, d, page):
-    """Shares of several long units, and of long beside very short ones: a warp's results of one unit after another
-    are joined by other warps while it goes on."""
+    """Shares of several long units, and of long beside very short ones: units that begin, end or lie in a warp's part
+    of a share, and such that span warps and CTAs."""
     g = np.random.default_rng(page)
     lens = [(1, int(x)) for x in g.integers(800, 4200, 48)]
     lens[5:5] = [(1, 3), (1, 0), (1, 64), (1, 65)] * 3
