@@ -98,6 +98,10 @@ __device__ __forceinline__ int32_t key_room(const AttnParams &P) {
     return static_cast<int32_t>(min(static_cast<int64_t>(P.a.max_pages) << P.page_shift, static_cast<int64_t>(kMaxKeys)));
 }
 
+// First key of the window of the row at position `pos`, which is negative for
+// rows before the first key: the widest window's differences would pass 32 bits there.
+__device__ __forceinline__ int32_t window_start(int32_t pos, int32_t window) { return pos >= window ? pos + 1 - window : 0; }
+
 __device__ __forceinline__ SplitReq split_req(const AttnParams &P, int r) {
     const df11_kv4_attention_args &A = P.a;
     SplitReq q{};
@@ -111,7 +115,7 @@ __device__ __forceinline__ SplitReq split_req(const AttnParams &P, int r) {
     q.tiles = (q.rows + kSplitCols - 1) / kSplitCols;
     q.kv = min(max(__ldg(A.kv_lens + r), 0), kMaxKeys);
     q.end = min(q.kv, key_room(P));
-    q.begin = A.window ? min(max(q.kv - q.n + 1 - A.window, 0), q.end) : 0;
+    q.begin = A.window ? min(window_start(q.kv - q.n, A.window), q.end) : 0;
     q.c_lo = q.begin / kSplitKeys;
     q.chunks = max((q.end + kSplitKeys - 1) / kSplitKeys - q.c_lo, 1);
     q.units = static_cast<int32_t>(P.kv_heads) * q.tiles;
@@ -157,8 +161,8 @@ __device__ __forceinline__ SplitSeen split_seen(const AttnParams &P, const Split
     SplitSeen s;
     s.all_hi = P.a.causal ? min(p0 + 1, at.q.end) : at.q.end;
     s.any_hi = P.a.causal ? min(p1 + 1, at.q.end) : at.q.end;
-    s.all_lo = P.a.window ? p1 + 1 - P.a.window : 0;
-    s.any_lo = P.a.window ? max(p0 + 1 - P.a.window, 0) : 0;
+    s.all_lo = P.a.window ? window_start(p1, P.a.window) : 0;
+    s.any_lo = P.a.window ? window_start(p0, P.a.window) : 0;
     return s;
 }
 
@@ -391,7 +395,7 @@ __device__ __forceinline__ void split_scores(const AttnParams &P, const uint8_t 
                 const uint32_t in = 16u * i + kg + (x & 2u);
                 const int key = key0 + static_cast<int>(in);
                 if (!(pages >> (in >> ES) & 1u) || key >= seen.any_hi || (P.a.causal && key > U.pos[x & 1]) ||
-                    (P.a.window && key <= U.pos[x & 1] - P.a.window))
+                    (P.a.window && U.pos[x & 1] - key >= P.a.window))
                     s[i][x] = -INFINITY;
             }
     }

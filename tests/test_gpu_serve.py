@@ -716,6 +716,19 @@ def test_widest_bounds(df11, n):
         p.check(o2, lse2)
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
+@pytest.mark.parametrize("hq,h,d", [(1, 1, 64), (2, 2, 128), (4, 1, 64)])
+def test_wide_windows_of_more_rows_than_keys(df11, hq, h, d, window):
+    """Rows at positions far below 0, whose distance to a wide window's start passes 32 bits: as without a window."""
+    lens = [(30, 20), (8, 5), (8, 4), (24, 20), (7, 0), (16, 33)] if hq == h else [(8, 5), (8, 4), (7, 0), (8, 33), (16, 2)]
+    p = Problem(df11, lens, hq, h, d, 16, seed=hq)
+    o, lse, err = p.run(window=window)
+    assert err.item() == 0
+    p.check(o, lse)
+    o2, lse2, _ = p.run()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("n", [2, 140])
 def test_rows_before_the_first_request(df11, n):
     """Row starts that begin past row 0: the rows before are left as they were."""
