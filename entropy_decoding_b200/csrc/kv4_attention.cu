@@ -808,6 +808,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
             break;
         }
         if (copied < share) {
+            __syncwarp();  // every lane has read `at`, which the next chunk's position replaces
             fence_proxy_async_smem();
             issue(st);
         }

@@ -512,6 +512,19 @@ def test_long_batches(df11, hq, h, d, page):
         assert err.item() == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("hq,h,d", [(24, 8, 64), (8, 8, 128)])
+def test_units_of_a_chunk_each(df11, hq, h, d):
+    """Every chunk ends a unit, whose columns are mostly empty: a stage's position is replaced right after the rows are
+    stored.  Again and again on one workspace, with equal bits."""
+    p = Problem(df11, [(1, 1 + (7 * r) % 64) for r in range(600)], hq, h, d, 64, seed=hq)
+    o, lse, err = p.run()
+    assert err.item() == 0
+    p.check(o, lse)
+    for _ in range(20):
+        o2, lse2, _ = p.run(ws=p.keep[-1], err=err)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2) and err.item() == 0
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_score_ranges(df11, n):
     """Scores far apart (one key takes all), tiny and huge queries and keys, a scale of 0 and a negative one."""
