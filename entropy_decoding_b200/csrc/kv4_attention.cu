@@ -180,6 +180,7 @@ struct SplitShared {
     SplitPos part_pos[kSplitWarps][2];
     int join_first[2], join_last[2], join[2];
     SplitPos join_pos[2];
+    int joins[2];  // of those, the ones that this CTA's arrival completes
     int dead;  // a wait gave up: what the CTA has is not joined
 };
 
@@ -900,18 +901,20 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
     }
     if (tid == 0) {
         __threadfence();  // the CTA's stores, seen at the barrier, before the arrivals
+        // into words of their own: other threads may still be reading S.join above
         for (int kind = 0; kind < 2; ++kind) {
+            S.joins[kind] = 0;
             if (!S.join[kind]) continue;
             int *counter = static_cast<int *>(A.workspace) + S.join_first[kind];
-            S.join[kind] = atomicAdd(counter, 1) == S.join_last[kind] - S.join_first[kind];
-            if (S.join[kind]) *counter = 0;
+            S.joins[kind] = atomicAdd(counter, 1) == S.join_last[kind] - S.join_first[kind];
+            if (S.joins[kind]) *counter = 0;
         }
         __threadfence();
     }
     __syncthreads();
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
-        if (!S.join[kind]) continue;
+        if (!S.joins[kind]) continue;
         const int b0 = S.join_first[kind], b1 = S.join_last[kind];
         for (int it = tid; it < kSplitCols * D / 4; it += kSplitThreads) {
             const int col = it / (D / 4), d = it % (D / 4) * 4;

@@ -525,6 +525,18 @@ def test_units_of_a_chunk_each(df11, hq, h, d):
         assert torch.equal(o, o2) and torch.equal(lse, lse2) and err.item() == 0
 
 
+@pytest.mark.parametrize("lens", [[(1, 20000)], [(1, 2100), (1, 2300), (1, 9000)]])
+def test_units_that_many_ctas_join(df11, lens):
+    """Every unit spans CTAs and every CTA has parts of up to two: which one arrives last differs, the bits do not."""
+    p = Problem(df11, lens, 8, 2, 64, 16, seed=len(lens))
+    o, lse, err = p.run()
+    assert err.item() == 0
+    p.check(o, lse)
+    for _ in range(50):
+        o2, lse2, _ = p.run(ws=p.keep[-1], err=err)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2) and err.item() == 0
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_score_ranges(df11, n):
     """Scores far apart (one key takes all), tiny and huge queries and keys, a scale of 0 and a negative one."""
