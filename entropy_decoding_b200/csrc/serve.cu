@@ -291,7 +291,10 @@ LaunchStatus launch_kv_extend(const df11_kv_extend_args &a, int *err, cudaStream
     return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;
 }
 
-LaunchStatus launch_qk_norm_rope(const df11_qk_norm_rope_args &a, cudaStream_t s) {
+LaunchStatus launch_qk_norm_rope(const df11_qk_norm_rope_args &args, cudaStream_t s) {
+    df11_qk_norm_rope_args a = args;
+    for (df11_rope_side *side : {&a.q, &a.k})
+        if (side->n_heads == 0) *side = {};  // nothing of an absent side is read, nor are its weights
     const int heads = a.q.n_heads + a.k.n_heads, per = kRopeThreads / (a.head_dim / 8);
     // few tokens: a CTA per token and group of heads, so that every element
     // has its own thread at once; many: one CTA per token, which makes the

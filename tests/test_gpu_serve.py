@@ -216,6 +216,24 @@ def test_rope_one_side(df11):
         assert np.abs(o.double().cpu().numpy().reshape(5, 2, 128) - y).max() <= 2.0 ** -8 * np.abs(y).max() + 1e-6
 
 
+def test_rope_absent_side_is_not_read(df11):
+    """Of a side without heads no pointer is checked, so none is followed: what it holds is any number."""
+    x = torch.randn(5, 256, device="cuda")
+    pos, freq = dev(np.arange(5), torch.int32), dev(0.1 * np.arange(64), torch.float64)
+    w = dev(1 + 0.1 * np.arange(128) / 128, torch.bfloat16)
+    absent = (2, 1, 2, 2, 1, 0)
+    outs = []
+    for left_out in (None, absent):
+        for first in (True, False):
+            o = torch.zeros(5, 256, dtype=torch.bfloat16, device="cuda")
+            side = (x.data_ptr(), 256, w.data_ptr(), o.data_ptr(), 256, 2)
+            q, k = (side, left_out) if first else (left_out, side)
+            df11.df11_qk_norm_rope(q, k, 5, 128, pos.data_ptr(), freq.data_ptr(), 128, stream=stream())
+            torch.cuda.synchronize()
+            outs.append(o)
+    assert outs[0].any() and all(torch.equal(o, outs[0]) for o in outs)
+
+
 # ------------------------------------------------------------------ the cache
 
 def device_cache(df11, c, pages=None):
