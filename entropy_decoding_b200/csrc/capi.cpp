@@ -112,11 +112,14 @@ df11_status check_attention(const df11_kv4_cache *c, const df11_kv4_attention_ar
     return DF11_OK;
 }
 
-df11_status check_rope_side(const df11_rope_side &s, int head_dim, bool fp32) {
+df11_status check_rope_side(const df11_rope_side &s, int n_tokens, int head_dim, bool fp32) {
     if (s.n_heads == 0) return DF11_OK;
     const uint64_t row = static_cast<uint64_t>(s.n_heads) * head_dim;
     if (!valid_rows(s.x, s.token_stride, row, fp32 ? 4 : 2) || !valid_rows(s.out, s.out_token_stride, row, 2) ||
         misaligned(s.weight, 16))
+        return DF11_EINVAL;
+    // in place, each element is written where it was read
+    if (s.x == s.out && n_tokens > 0 && (fp32 || (n_tokens > 1 && s.token_stride != s.out_token_stride)))
         return DF11_EINVAL;
     return DF11_OK;
 }
@@ -843,7 +846,7 @@ df11_status df11_qk_norm_rope(const df11_qk_norm_rope_args *args, df11_stream st
     if (a.rot_dim && (!a.positions || !a.inv_freq || misaligned(a.positions, 4) || misaligned(a.inv_freq, 8)))
         return DF11_EINVAL;
     for (const df11_rope_side *s : {&a.q, &a.k}) {
-        const df11_status st = check_rope_side(*s, a.head_dim, a.dtype == DF11_FP32);
+        const df11_status st = check_rope_side(*s, a.n_tokens, a.head_dim, a.dtype == DF11_FP32);
         if (st != DF11_OK) return st;
     }
     if (a.n_tokens == 0 || a.q.n_heads + a.k.n_heads == 0) return DF11_OK;

@@ -688,7 +688,7 @@ typedef struct {
     const void *x;             /* device, DF11_FP32 or DF11_BF16, 16-byte aligned rows */
     uint64_t token_stride;     /* elements, at least n_heads * head_dim */
     const void *weight;        /* device, head_dim BF16 norm weights, or NULL: no norm */
-    void *out;                 /* device, BF16, 16-byte aligned rows; with BF16 x it may be x itself */
+    void *out;                 /* device, BF16, 16-byte aligned rows; with BF16 x and the same stride it may be x itself */
     uint64_t out_token_stride;
     int32_t n_heads;           /* 0: this side is absent */
 } df11_rope_side;
@@ -711,7 +711,8 @@ typedef struct {
  * a head's head_dim elements (left out when weight is NULL), then each pair
  * (a, b) -> (a cos - b sin, b cos + a sin), the angle position * inv_freq in
  * 64 bits; FP32 throughout, rounded to BF16 once.
- * Errors: DF11_EINVAL (NULL or misaligned pointer or stride, sizes, eps),
+ * Errors: DF11_EINVAL (NULL or misaligned pointer or stride, sizes, eps, out at
+ * x in another type or at another stride),
  * DF11_EUNSUPPORTED (head_dim), DF11_ECUDA. */
 df11_status df11_qk_norm_rope(const df11_qk_norm_rope_args *args, df11_stream stream);
 

@@ -125,6 +125,15 @@ def test_rope_refusals(df11):
     df11.df11_qk_norm_rope(None, None, 3, 128, A, A, 128)
 
 
+def test_rope_in_place_refusals(df11):
+    """In place, a row is written where it was read: neither at another stride nor in another type."""
+    good = dict(q=(A, 512, A, A, 512, 4), k=None, n_tokens=3, head_dim=128, positions_ptr=A, inv_freq_ptr=A, rot_dim=128,
+                dtype="bf16")
+    for b in [dict(q=(A, 512, A, A, 520, 4)), dict(q=(A, 520, 0, A, 512, 4)), dict(q=None, k=(A, 128, A, A, 136, 1)),
+              dict(dtype="fp32"), dict(dtype="fp32", n_tokens=1)]:
+        refused(df11, df11.DF11_EINVAL, df11.df11_qk_norm_rope, **{**good, **b})
+
+
 def bad_caches(df11):
     ok = dict(pages=A, n_pages=4, page_size=16, n_heads=2, head_dim=128, k_scale=1.0, v_scale=1.0)
     E, U = df11.DF11_EINVAL, df11.DF11_EUNSUPPORTED
