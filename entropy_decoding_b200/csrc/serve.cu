@@ -27,7 +27,9 @@ __device__ __forceinline__ void flag(int *err, uint32_t bits) {
 // them.  A row finds its request by bisection among the scanned starts; the
 // row that starts a page is the one that writes the page into the block table,
 // and every row computes its page's id from the free stack itself, so no
-// thread reads what another writes.  Bound by the launch and two rounds through
+// thread reads what another writes.  Pages are those that the table has room
+// for; where rows are cut off at max_tokens, the first CTA writes the pages
+// that they would have started, so every page taken is in the table.  Bound by the launch and two rounds through
 // L2: 3.1 us for 128 requests of a token each, 4.9 us for 509 with up to 2048
 // new tokens each.
 constexpr int kExtendThreads = 512;
@@ -49,7 +51,7 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const df11_kv
     const bool first = blockIdx.x == 0;
     const int64_t t_end = (static_cast<int64_t>(blockIdx.x) + 1) * kExtendThreads, t = t_end - kExtendThreads + tid;
     const int32_t mask = A.page_size - 1;
-    const int64_t n_free = max(*A.n_free, 0);
+    const int64_t n_free = max(*A.n_free, 0), room = A.max_pages;
     uint32_t bad = 0;
     int64_t rows = 0, pages = 0;  // of the requests before this tile
     for (int base = 0; base < A.n_reqs && (first || rows < t_end); base += kExtendThreads) {
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const df11_kv
             nw = max(nw, 0);
         }
         const int64_t len = static_cast<int64_t>(kv) + nw;
-        const int64_t np = ((len + mask) >> shift) - ((static_cast<int64_t>(kv) + mask) >> shift);
+        const int64_t np = min((len + mask) >> shift, room) - min((static_cast<int64_t>(kv) + mask) >> shift, room);
         int64_t ri = warp_incl(nw, lane), pi = warp_incl(np, lane);
         if (lane == 31) {
             s_sum[0][warp] = ri;
@@ -112,6 +114,19 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const df11_kv
             if (id < 0) bad |= DF11_DEV_ERR_PAGES;
             A.slots[t] = id < 0 ? -1 : (static_cast<int64_t>(id) << shift) + (pos & mask);
             A.positions[t] = static_cast<int32_t>(min(pos, static_cast<int64_t>(INT32_MAX)));
+        }
+        if (first && rows + all_rows > A.max_tokens) {
+            for (int i = 0; i < cnt; ++i) {
+                const int64_t held = (static_cast<int64_t>(s_kv[i]) + mask) >> shift;
+                const int64_t end = min((s_kv[i] + static_cast<int64_t>(max(A.new_lens[base + i], 0)) + mask) >> shift, room);
+                // page p starts at row s_row + (p << shift) - s_kv; the first such row that is cut off
+                const int64_t cut = (A.max_tokens - s_row[i] + s_kv[i] + mask) >> shift;
+                for (int64_t pg = max(held, cut) + tid; pg < end; pg += kExtendThreads) {
+                    const int64_t taken = s_page[i] + pg - held;
+                    A.block_table[static_cast<int64_t>(base + i) * A.max_pages + pg] =
+                        taken < n_free ? A.free_pages[n_free - 1 - taken] : -1;
+                }
+            }
         }
         rows += all_rows;
         pages += all_pages;

@@ -657,7 +657,8 @@ typedef struct {
     const int32_t *free_pages; /* stack of free page ids, the top at *n_free - 1 */
     const int32_t *n_free;
     int32_t *block_table;      /* n_reqs x max_pages, in and out: entries of the pages held stay, entries of
-                                  the pages taken are written, the rest is left as it was */
+                                  the pages taken are written (-1 where the stack ran out), the rest is left
+                                  as it was */
     int32_t page_size;         /* tokens per page: 16, 32, 64 or 128 */
     int32_t max_tokens;        /* entries of slots and positions */
     int32_t *kv_lens_out;      /* n_reqs: kv_lens + new_lens */
@@ -670,14 +671,18 @@ typedef struct {
 
 /* Pages, block tables, slots and positions of one step, from the requests'
  * lengths, in ONE launch.  Request by request in order, and within a request
- * in order of position, each page that a new token starts is the top of the
- * free stack.  free_pages and *n_free are only read: the same call again
- * gives the same result, and the next step passes kv_lens_out and n_free_out
- * as its inputs.
+ * in order of position, each page that a new token starts, as far as the
+ * table has room, is the top of the free stack.  free_pages and *n_free are
+ * only read: the same call again gives the same result, and the next step
+ * passes kv_lens_out and n_free_out as its inputs.
  * DF11_DEV_ERR_PAGES: the free stack ran out, a row is longer than
  * max_pages, or a held page's entry is negative (those rows get slot -1).
  * DF11_DEV_ERR_AUX: a negative length (taken as 0), or more rows than
  * max_tokens (q_start is cut there, the rows past it have no slot).
+ * After either, kv_lens_out still counts every new token, and every page that
+ * n_free_out no longer counts is in the table; but what has no slot has no
+ * place in the cache, so the step is to be done again, from the inputs it
+ * had, with room for it.
  * Errors: DF11_EINVAL (NULL or misaligned pointer, sizes), DF11_ECUDA. */
 df11_status df11_kv_extend(const df11_kv_extend_args *args, int *dev_err_flag, df11_stream stream);
 

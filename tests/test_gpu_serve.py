@@ -110,6 +110,61 @@ def test_extend_reports_what_does_not_fit(df11):
     assert err == A | P and got[2] == [0, 3, 3, 3] and got[3] == [32, 33, 34] and got[5] == 0
 
 
+def extend_with_limits(kv, new, free, table, page, max_tokens):
+    """ref.extend for a table of any width, a stack that may run out and rows past max_tokens."""
+    table, stack = [list(map(int, row)) for row in table], list(map(int, free))
+    kv_out, q_start, slots, pos, pages = [], [0], [], [], False
+    for r, (a, n) in enumerate(zip(map(int, kv), map(int, new))):
+        for p in range(a, a + n):
+            at, room = p // page, p // page < len(table[r])
+            if room and p % page == 0:
+                table[r][at] = stack.pop() if stack else -1
+            if not room or table[r][at] < 0:
+                pages = True
+            slots.append(table[r][at] * page + p % page if room and table[r][at] >= 0 else -1)
+            pos.append(p)
+        kv_out.append(a + n)
+        q_start.append(min(len(slots), max_tokens))
+    pad, over = max(max_tokens - len(slots), 0), len(slots) > max_tokens
+    return (table, kv_out, q_start, (slots + [-1] * pad)[:max_tokens], (pos + [0] * pad)[:max_tokens], len(stack)), pages, over
+
+
+@pytest.mark.parametrize("reqs,page,new_max", [(2, 16, 60), (40, 16, 50), (700, 32, 90), (5, 128, 1500)])
+@pytest.mark.parametrize("short", ["rows", "table", "pages", "all"])
+def test_extend_loses_no_page(df11, reqs, page, new_max, short):
+    """What does not fit is flagged, every page taken from the stack is in the table all the same, and the next step
+    finds it there."""
+    g = np.random.default_rng(reqs)
+    kv, new = g.integers(0, 3 * page, reqs), g.integers(0, new_max + 1, reqs)
+    held = -(-kv // page)
+    w = int(-(-(kv + new).max() // page)) + 1
+    if short in ("table", "all"):
+        w = max(int(held.max()), w // 2)
+    ids = g.permutation(int(held.sum()) + int((-(-(kv + new) // page) - held).sum()) + 2 * reqs)
+    table, at = np.full((reqs, w), -7), 0
+    for r in range(reqs):
+        table[r, :held[r]] = ids[at:at + held[r]]
+        at += held[r]
+    free = ids[at:]
+    if short in ("pages", "all"):
+        free = free[-max(1, int((-(-(kv + new) // page) - held).sum()) // 2):]
+    max_tokens = int(new.sum()) // 2 if short in ("rows", "all") else int(new.sum()) + 3
+    got, err = run_extend(df11, kv, new, free, len(free), table, page, max_tokens)
+    want, pages, over = extend_with_limits(kv, new, free, table, page, max_tokens)
+    names = ("table", "kv_out", "q_start", "slots", "positions", "n_free")
+    for name, a, b in zip(names, got, want):
+        assert a == b, name
+    assert err == df11.DEV_ERR_PAGES * pages + df11.DEV_ERR_AUX * over
+    taken = [p for row, h in zip(got[0], held) for p in row[h:] if p >= 0]
+    assert sorted(taken + list(free[:got[5]])) == sorted(free)
+    # one more token for each request
+    got2, err2 = run_extend(df11, got[1], [1] * reqs, free, got[5], got[0], page, reqs)
+    want2, pages, over = extend_with_limits(want[1], [1] * reqs, free[:want[5]], want[0], page, reqs)
+    for name, a, b in zip(names, got2, want2):
+        assert a == b, name
+    assert err2 == df11.DEV_ERR_PAGES * pages and not over
+
+
 def test_extend_repeats_and_chains(df11):
     """The same call twice gives the same result; the next step takes the outputs as inputs."""
     i32, page, n = torch.int32, 16, 5
