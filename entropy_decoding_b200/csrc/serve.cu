@@ -301,7 +301,7 @@ void launch_rope(const df11_qk_norm_rope_args &a, dim3 grid, cudaStream_t s) {
 LaunchStatus launch_kv_extend(const df11_kv_extend_args &a, int *err, cudaStream_t s) {
     int shift = 0;
     while ((1 << shift) < a.page_size) ++shift;
-    const unsigned grid = a.max_tokens > 0 ? (a.max_tokens + kExtendThreads - 1) / kExtendThreads : 1;
+    const unsigned grid = a.max_tokens > 0 ? (static_cast<unsigned>(a.max_tokens) + kExtendThreads - 1) / kExtendThreads : 1;
     kv_extend_kernel<<<grid, kExtendThreads, 0, s>>>(a, shift, err);
     return cudaGetLastError() == cudaSuccess ? LaunchStatus::kOk : LaunchStatus::kCuda;
 }

@@ -165,6 +165,25 @@ def test_extend_loses_no_page(df11, reqs, page, new_max, short):
     assert err2 == df11.DEV_ERR_PAGES * pages and not over
 
 
+@pytest.mark.slow
+def test_extend_most_rows(df11):
+    """As many rows as their count can say (26 GB of slots and positions), all but three of them padding."""
+    n = 2 ** 31 - 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    slots, pos = torch.full((n,), 7, dtype=torch.int64, device="cuda"), torch.full((n,), 7, **i32)
+    kv, new, free, nf, table = (torch.tensor(x, **i32) for x in ([0], [3], [5], [1], [-1]))
+    kvo, qs, nfo, err = (torch.zeros(k, **i32) for k in (1, 2, 1, 1))
+    df11.df11_kv_extend(kv.data_ptr(), new.data_ptr(), 1, free.data_ptr(), nf.data_ptr(), table.data_ptr(), 1, 16,
+                        kvo.data_ptr(), qs.data_ptr(), slots.data_ptr(), pos.data_ptr(), n, nfo.data_ptr(), err.data_ptr(),
+                        stream())
+    torch.cuda.synchronize()
+    assert err.item() == 0 and kvo.item() == 3 and qs.tolist() == [0, 3] and nfo.item() == 0 and table.item() == 5
+    assert slots[:3].tolist() == [80, 81, 82] and pos[:3].tolist() == [0, 1, 2]
+    for x, want in ((slots, -1), (pos, 0)):
+        lo, hi = x[3:].aminmax()
+        assert lo.item() == want and hi.item() == want
+
+
 def test_extend_repeats_and_chains(df11):
     """The same call twice gives the same result; the next step takes the outputs as inputs."""
     i32, page, n = torch.int32, 16, 5
