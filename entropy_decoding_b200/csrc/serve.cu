@@ -299,6 +299,7 @@ void launch_rope(const df11_qk_norm_rope_args &a, dim3 grid, cudaStream_t s) {
 }  // namespace
 
 LaunchStatus launch_kv_extend(const df11_kv_extend_args &a, int *err, cudaStream_t s) {
+    if (a.n_reqs > INT_MAX - kExtendThreads) return LaunchStatus::kUnsupported;  // a tile past them would pass 31 bits
     int shift = 0;
     while ((1 << shift) < a.page_size) ++shift;
     const unsigned grid = a.max_tokens > 0 ? (static_cast<unsigned>(a.max_tokens) + kExtendThreads - 1) / kExtendThreads : 1;

@@ -683,7 +683,8 @@ typedef struct {
  * n_free_out no longer counts is in the table; but what has no slot has no
  * place in the cache, so the step is to be done again, from the inputs it
  * had, with room for it.
- * Errors: DF11_EINVAL (NULL or misaligned pointer, sizes), DF11_ECUDA. */
+ * Errors: DF11_EINVAL (NULL or misaligned pointer, sizes), DF11_EUNSUPPORTED
+ * (2^31 - 512 requests or more), DF11_ECUDA. */
 df11_status df11_kv_extend(const df11_kv_extend_args *args, int *dev_err_flag, df11_stream stream);
 
 /* One side (queries or keys) of df11_qk_norm_rope: element (t, h, d) of x at

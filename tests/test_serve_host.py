@@ -102,6 +102,15 @@ def test_extend_refusals(df11):
         refused(df11, df11.DF11_EINVAL, df11.df11_kv_extend, **{**good, **b})
 
 
+def test_extend_refuses_what_it_cannot_count(df11):
+    """The kernel counts requests in 31 bits, 512 at a time."""
+    args = dict(kv_lens_ptr=A, new_lens_ptr=A, free_pages_ptr=A, n_free_ptr=A, block_table_ptr=A, max_pages=4,
+                page_size=16, kv_lens_out_ptr=A, q_start_ptr=A, slots_ptr=A, positions_ptr=A, max_tokens=8,
+                n_free_out_ptr=A)
+    for n in (2 ** 31 - 512, 2 ** 31 - 1):
+        refused(df11, df11.DF11_EUNSUPPORTED, df11.df11_kv_extend, n_reqs=n, **args)
+
+
 def test_rope_refusals(df11):
     side = (A, 512, A, A, 512, 4)
     good = dict(q=side, k=(A, 512, 0, A, 128, 1), n_tokens=3, head_dim=128, positions_ptr=A, inv_freq_ptr=A, rot_dim=128)
