@@ -537,6 +537,9 @@ def df11_decode_gemm_launch_shape(mats, m: int):
 
 def _packer(cls):
     """Packs the fields of a structure, those of structures inside it one after another, into its bytes."""
+    def types(c):
+        return [x for _, t in c._fields_ for x in (types(t) if issubclass(t, ctypes.Structure) else [t])]
+
     def layout(c):
         fmt, at = "", 0
         for name, t in c._fields_:
@@ -546,7 +549,15 @@ def _packer(cls):
             fmt, at = fmt + "x" * (field.offset - at) + inner, field.offset + n
         return fmt + "x" * (ctypes.sizeof(c) - at), ctypes.sizeof(c)
 
-    return struct.Struct("=" + layout(cls)[0]).pack
+    pack = struct.Struct("=" + layout(cls)[0]).pack
+
+    def packed(*fields):
+        try:
+            return pack(*fields)
+        except struct.error:  # NULL pointers among them, or what is no field's value, which then raises again
+            return pack(*[0 if f is None and t is _P else f for f, t in zip(fields, types(cls))])
+
+    return packed
 
 
 def _packed(name, *before):
@@ -618,7 +629,7 @@ def df11_kv4_attention(cache: Kv4Cache, q_ptr: int, q_token_stride: int, o_ptr: 
                        workspace_bytes: int, causal: bool = True, window: int = 0, lse_ptr: int | None = None,
                        err_ptr: int | None = None, stream: int = 0):
     st = _kv4_attention(cache, _attention_args(q_ptr, q_token_stride, o_ptr, o_token_stride, lse_ptr or 0, q_start_ptr,
-                                               kv_lens_ptr, block_table_ptr or 0, n_reqs, max_pages, n_tokens, n_q_heads,
+                                               kv_lens_ptr, block_table_ptr, n_reqs, max_pages, n_tokens, n_q_heads,
                                                max_q_len, causal, window, scale, workspace_ptr, workspace_bytes),
                         err_ptr, stream)
     if st:

@@ -143,6 +143,35 @@ def test_rope_in_place_refusals(df11):
         refused(df11, df11.DF11_EINVAL, df11.df11_qk_norm_rope, **{**good, **b})
 
 
+def test_none_is_null(df11):
+    """None for a pointer is a NULL pointer, in each place: refused by the library where one is needed, else taken."""
+    E = df11.DF11_EINVAL
+    extend = [A, A, 2, A, A, A, 4, 16, A, A, A, A, 8, A]
+    for i in (0, 1, 3, 4, 5, 8, 9, 10, 11, 13):
+        refused(df11, E, df11.df11_kv_extend, *extend[:i], None, *extend[i + 1:])
+    side = (A, 512, None, A, 512, 4)
+    for q in ((None, *side[1:]), (*side[:3], None, *side[4:])):
+        refused(df11, E, df11.df11_qk_norm_rope, q, None, 3, 128, A, A, 128)
+    refused(df11, E, df11.df11_qk_norm_rope, side, None, 3, 128, None, A, 128)
+    refused(df11, E, df11.df11_qk_norm_rope, side, None, 3, 128, A, None, 128)
+    df11.df11_qk_norm_rope(side, None, 0, 128, None, None, 0)
+    c = cache(df11)
+    attend = dict(q_ptr=A, q_token_stride=512, o_ptr=A, o_token_stride=512, n_q_heads=4, q_start_ptr=A, kv_lens_ptr=A,
+                  block_table_ptr=A, n_reqs=2, max_pages=4, n_tokens=5, max_q_len=3, scale=0.1, workspace_ptr=A,
+                  workspace_bytes=1 << 40)
+    for name in ("q_ptr", "o_ptr", "q_start_ptr", "kv_lens_ptr", "block_table_ptr", "workspace_ptr"):
+        refused(df11, E, df11.df11_kv4_attention, c, **{**attend, name: None})
+    for name in ("k_ptr", "v_ptr", "slots_ptr"):
+        refused(df11, E, df11.df11_kv4_append, c, **{**dict(k_ptr=A, k_token_stride=256, v_ptr=A, v_token_stride=256,
+                                                            slots_ptr=A, n_tokens=3), name: None})
+    refused(df11, E, df11.df11_kv4_gather, c, None, 3, A, A)
+    # what is no pointer, or a count that is none, stays an error of its own
+    for wrong in (["x", *extend[1:]], [*extend[:2], None, *extend[3:]]):
+        with pytest.raises(Exception) as e:
+            df11.df11_kv_extend(*wrong)
+        assert not isinstance(e.value, df11.Df11Error)
+
+
 def bad_caches(df11):
     ok = dict(pages=A, n_pages=4, page_size=16, n_heads=2, head_dim=128, k_scale=1.0, v_scale=1.0)
     E, U = df11.DF11_EINVAL, df11.DF11_EUNSUPPORTED
