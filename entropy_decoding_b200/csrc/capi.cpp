@@ -903,6 +903,8 @@ df11_status df11_kv4_attention(const df11_kv4_cache *cache, const df11_kv4_atten
     if (a.causal < 0 || a.causal > 1 || a.window < 0 || (a.window && !a.causal) || !std::isfinite(a.scale) ||
         a.max_pages < 0)
         return DF11_EINVAL;
+    // the scores' factor, in log2 units, as the kernels make it
+    if (!std::isfinite(a.scale * cache->k_scale * 1.44269504088896341f)) return DF11_EINVAL;
     if (a.n_reqs == 0 || a.n_tokens == 0 || a.max_q_len == 0) return DF11_OK;
     const uint64_t row = static_cast<uint64_t>(a.n_q_heads) * cache->head_dim;
     if (!valid_rows(a.q, a.q_token_stride, row, 2) || !valid_rows(a.o, a.o_token_stride, row, 2) || !a.q_start ||

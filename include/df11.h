@@ -786,7 +786,8 @@ typedef struct {
     int32_t max_q_len;          /* upper bound on a request's rows */
     int32_t causal;             /* 1: row i of n sees keys 0 .. kv_len - n + i; 0: every key */
     int32_t window;             /* with causal: only the last `window` of those; 0 = all */
-    float scale;                /* of the scores, finite */
+    float scale;                /* of the scores, finite; scale * k_scale * log2(e) is one FP32 factor of a
+                                   row's scores and has to be finite too */
     void *workspace;            /* df11_kv4_attention_workspace_bytes, 16-byte aligned; all zero before its
                                    first use, after which every call leaves what the next one needs.
                                    Calls that may run at the same time need one each; zero it again

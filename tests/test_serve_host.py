@@ -236,6 +236,16 @@ def test_attention_refusals(df11):
         refused(df11, df11.DF11_EUNSUPPORTED, df11.df11_kv4_attention, c, **{**good, **b})
 
 
+def test_attention_refuses_scales_past_fp32(df11):
+    """The scores' factor is the product of two scales, each finite: where that is not, 0 times it would be NaN."""
+    good = dict(q_ptr=A, q_token_stride=512, o_ptr=A, o_token_stride=512, n_q_heads=4, q_start_ptr=A, kv_lens_ptr=A,
+                block_table_ptr=A, n_reqs=2, max_pages=4, n_tokens=5, max_q_len=3, workspace_ptr=A, workspace_bytes=1 << 40)
+    for k, scale in ((1e30, 1e10), (1e30, -1e10), (1.0, 3e38), (3e38, 1.0), (1e38, 3.0)):
+        refused(df11, df11.DF11_EINVAL, df11.df11_kv4_attention, cache(df11, k_scale=k), scale=scale, **good)
+    for k, scale in ((1e30, 1e7), (2e38, -1.0), (1e38, 1e-38), (1e-30, 1e-30)):  # nothing to do, but no error either
+        df11.df11_kv4_attention(cache(df11, k_scale=k), scale=scale, **{**good, "n_tokens": 0})
+
+
 # ------------------------------------------------------------------ the reference itself
 
 def test_reference_quantizer_by_hand():
