@@ -18,10 +18,11 @@ namespace {
 // Neighbouring threads take the 4 tokens (whose 8-byte pieces of V codes and
 // bytes of V scales are neighbours where the tokens are), then the blocks of a
 // row, which are contiguous in the rows and, within a head, in the K codes.
-// 16,384 tokens of 8 heads of 128 (86 MB each way): append 17 us, 5.0 TB/s, bound
-// by latency and instructions (57 % of the issue slots, the quotients most of
-// them); gather 15 us, 5.7 TB/s.  CTAs of 128 threads take 0.7 us less of the 32,
-// and a step of 64 tokens 5.6 us, not 4.4.
+// 16,384 tokens of 8 heads of 128 (86 MB each way) appended and then gathered
+// take 33 us, 5.2 TB/s; each again and again, its data partly in L2, 16 and 13.
+// Append is bound by latency and instructions (61 % of the issue slots, the
+// quotients most of them).  CTAs of 128 threads took 0.7 us less of the two, and a
+// step of 64 tokens 5.6 us, not 4.4.
 constexpr int kKv4Threads = 256;
 constexpr int kKv4Tokens = 4;
 

@@ -46,25 +46,27 @@ struct AttnParams {
 // columns are used; here nothing decoded is ever stored.
 // 64 requests of 256 to 16384 keys (8 cache heads of 128, groups of 4, 651 MB)
 // take 148 us, 4.4 TB/s; two of 98301 to 131072 keys 64 us.  Bound by instructions
-// at 3 warps a scheduler (some 1200 for a chunk: 512 conversions, 512 products
-// with the scales, 64 MMAs); copies alone took 118 us.
+// at 3 warps a scheduler: 1170 for a chunk with its part of the unit, of which
+// 256 are conversions, 256 products with the scales and 64 MMAs; copies alone
+// took 118 us.
 constexpr int kSplitWarps = 12;
 constexpr int kSplitThreads = 32 * kSplitWarps;
 constexpr int kSplitCols = 8;      // rows of a unit
 constexpr int kSplitKeys = 64;     // keys of a chunk: a warp's step
 constexpr int kSplitStages = 2;    // chunks that a warp has room for
 // Rows (tokens x heads of a group) of a request that go this way at most: the
-// time goes with them in steps of 8, the other kernel's hardly.  32 requests on
-// 2000 keys of 8 heads of 128 take 86 us with 32 rows each, 131 with 48 and 165
-// with 64, the other kernel 90; one request alone 16 us with 32 to 64 rows, the
-// other kernel 23 (on 8000 keys: 19 to 29, and 34).
+// time goes with them in steps of 8, since each 8 rows decode the keys again,
+// the other kernel's hardly.  32 requests on 2000 keys of 8 heads of 128 take 77
+// us with 32 rows each, 110 with 48 and 138 with 64, the other kernel 91; one
+// request alone 15 to 17 us with 32 to 64 rows, the other kernel 23 (on 8000
+// keys: 21 to 28, and 34).
 constexpr int kSplitRows = 32, kSplitRowsFew = 64;
 constexpr int kSplitFew = 16;  // requests times cache heads, at most, with the second bound
 // What a unit costs a CTA beside its chunks (queries, joins), in chunks: shares
 // are equal in this measure, in which a unit starts with so many empty places.
 // With 4, 8 and 16, 64 requests of 256 to 16384 keys (8 cache heads of 128,
-// groups of 4) take 146, 146 and 148 us, 2 of 98301 to 131072 keys 66, 64 and 64,
-// one of 12000 18, 16 and 16, and 8 of 1000 16, 15 and 14.
+// groups of 4) take 147, 146 and 149 us, 2 of 98301 to 131072 keys 66, 65 and 64,
+// one of 12000 17, 16 and 16, and 8 of 1000 16, 15 and 14.
 constexpr int kSplitUnitCost = 16;
 constexpr int32_t kMaxKeys = INT32_MAX - 255;
 
@@ -234,8 +236,8 @@ struct SplitUnit {
 
 // Loads the unit's queries: thread (g, t) takes elements [t D / 4, (t + 1) D /
 // 4) of column g.  A column is scaled by a power of two that brings its
-// largest element into [1, 2): FP16 holds it without loss but for elements
-// below 2^-24 of that one.
+// largest element into [1, 2): FP16 holds it to 2^-25 of that one, which for
+// BF16's 8 bits is without loss down to 2^-17 of it.
 template <int D>
 __device__ __forceinline__ void split_load_unit(const AttnParams &P, const SplitPos &at, int lane, SplitUnit<D> &U) {
     const df11_kv4_attention_args &A = P.a;
@@ -620,11 +622,13 @@ struct SplitJoin {
 // Whether units of at most `longest` chunks are not divided between CTAs, whose
 // shares are of `share` places: units of a chunk a warp, and those that come to
 // one or a few a CTA.  A join of CTAs takes 1 to 3 us, and the last CTA to finish
-// has up to a unit more.  8 heads of 128, whole and divided: one token on 500
-// keys 11.1 and 11.8 us, on 2000 15.9 and 12.5; 8 tokens on 1000 keys each 13.5
-// and 15.3, on 3000 20.5 and 18.8; 32 on 2000 27.4 and 30.3; 100 on 1000 43.9 and
-// 48.5, on 2000 66.7 and 69.0, on 3000 92.4 and 89.7; 8 with 24 rows each on
-// 8000 keys 74 and 58.
+// has up to a unit more.  8 heads of 128, with the kernel built for whole and
+// for divided units: one token on 500 keys 11.0 and 12.1 us, on 1000 12.5 and
+// 12.5, on 2000 15.9 and 12.6; 8 tokens on 1000 keys each 13.4 and 15.3, on 3000
+// 20.4 and 18.6; 32 on 2000 27.3 and 30.3; 100 on 1000 43.7 and 48.2, on 2000 66.8
+// and 69.5, on 3000 92.4 and 90.4; 8 with 24 rows each on 8000 keys 74 and 57.  With
+// the rule in it the kernel takes the better side's time, up to 0.9 us more (one
+// token on 1000 keys: 13.3).
 __device__ __forceinline__ bool split_whole(int longest, int share) {
     return longest <= kSplitWarps || (longest <= 4 * kSplitWarps && longest <= share + share / 4 && share <= 320);
 }
@@ -1205,8 +1209,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
 
     // ---- this CTA's request and rows: pairs of tiles in the order of the most
     // keys that a row of the request sees, a request's last rows first (the
-    // last to start should not be long: 5 prompt chunks of 133 to 765 tokens on
-    // 209 to 7278 keys take 49 us so, and 60 in the order of the requests)
+    // last to start should not be long: 6 prompt chunks of 21 to 765 tokens on
+    // 209 to 7278 keys take 50 us so, and 62 in the order of the requests)
     const uint32_t place = SHARED ? blockIdx.x / P.parts : blockIdx.x;
     const int want = static_cast<int>(place / P.kv_heads), head = static_cast<int>(place % P.kv_heads);
     int64_t all = 0;  // 64 bits: row starts that are no ascending ones could count the same rows many times
@@ -1488,47 +1492,47 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
             else prefill_join<D, 2>(P, W, head, warp, lane, so, sp);
             cluster_sync();
         } else if (part == 0) {
-        // Rows out of TMEM into the tile's query operand, which no MMA reads any
-        // more (a thread its own row), and from there to o, a row's chunks on
-        // D / 8 lanes.  l == 0: the row saw no key, whatever the accumulator holds.
-        const float inv = !run ? 0.0f : l > 0.0f ? P.v_scale / l : l;  // NaN stays NaN
-        if (steps) {
+            // Rows out of TMEM into the tile's query operand, which no MMA reads any
+            // more (a thread its own row), and from there to o, a row's chunks on
+            // D / 8 lanes.  l == 0: the row saw no key, whatever the accumulator holds.
+            const float inv = !run ? 0.0f : l > 0.0f ? P.v_scale / l : l;  // NaN stays NaN
+            if (steps) {
 #pragma unroll
-            for (int i = 0; i < D; i += 16) {
-                uint32_t o[16];
-                tc_ld16(o_col + i, o);
-                tc_wait_ld();
+                for (int i = 0; i < D; i += 16) {
+                    uint32_t o[16];
+                    tc_ld16(o_col + i, o);
+                    tc_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 16; y += 8) {
-                    uint32_t w[4];
+                    for (int y = 0; y < 16; y += 8) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        w[z] = l == 0.0f ? 0u
-                                         : bf16x2_of(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
-                    const int c = (i + y) / 8;
-                    *reinterpret_cast<uint4 *>(S.q[x] + (c / 8) * (kPrefillTile * 128) + swz_chunk(r, c % 8)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int z = 0; z < 4; ++z)
+                            w[z] = l == 0.0f ? 0u
+                                             : bf16x2_of(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
+                        const int c = (i + y) / 8;
+                        *reinterpret_cast<uint4 *>(S.q[x] + (c / 8) * (kPrefillTile * 128) + swz_chunk(r, c % 8)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                __syncwarp();
+            }
+            {
+                constexpr int kLanes = D / 8, kAt = 32 / kLanes;
+                const int c = lane % kLanes;
+#pragma unroll 4
+                for (int i = 0; i < 32 / kAt; ++i) {
+                    const int rt = (warp & 3) * 32 + i * kAt + lane / kLanes, rw = W.row0 + x * kPrefillTile + rt;
+                    if (rw >= W.rows) continue;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (steps)
+                        v = *reinterpret_cast<const uint4 *>(S.q[x] + (c / 8) * (kPrefillTile * 128) + swz_chunk(rt, c % 8));
+                    *reinterpret_cast<uint4 *>(
+                        static_cast<uint16_t *>(A.o) +
+                        static_cast<int64_t>(W.q0 + rw / group) * static_cast<int64_t>(A.o_token_stride) +
+                        (head * group + rw % group) * D + c * 8) = v;
                 }
             }
-            __syncwarp();
-        }
-        {
-            constexpr int kLanes = D / 8, kAt = 32 / kLanes;
-            const int c = lane % kLanes;
-#pragma unroll 4
-            for (int i = 0; i < 32 / kAt; ++i) {
-                const int rt = (warp & 3) * 32 + i * kAt + lane / kLanes, rw = W.row0 + x * kPrefillTile + rt;
-                if (rw >= W.rows) continue;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (steps)
-                    v = *reinterpret_cast<const uint4 *>(S.q[x] + (c / 8) * (kPrefillTile * 128) + swz_chunk(rt, c % 8));
-                *reinterpret_cast<uint4 *>(
-                    static_cast<uint16_t *>(A.o) +
-                    static_cast<int64_t>(W.q0 + rw / group) * static_cast<int64_t>(A.o_token_stride) +
-                    (head * group + rw % group) * D + c * 8) = v;
-            }
-        }
-        if (live && A.lse) A.lse[token * A.n_q_heads + hq] = lse_of(m, l);
+            if (live && A.lse) A.lse[token * A.n_q_heads + hq] = lse_of(m, l);
         }
         tc_fence_before();
     } else if (warp < 12) {
@@ -1896,13 +1900,13 @@ LaunchStatus launch_kv4_attention(const df11_kv4_cache &c, const df11_kv4_attent
         pairs = std::min((rows + some * (2 * kPrefillTile - 1)) / (2 * kPrefillTile), some * most);
         // where clusters of CTAs, one for each pair and head, run all at the same
         // time, they share the keys: 85 tokens in groups of 3 against 8192 keys of
-        // 8 heads take 154 us alone (D = 64; 168 for D = 128), 31 (38) with 8
+        // 8 heads take 135 us alone (D = 64; 139 for D = 128), 32 (39) with 8
         const int64_t steps = ((static_cast<int64_t>(a.max_pages) << P.page_shift) + kPrefillTile - 1) / kPrefillTile;
         for (int i = 1; pairs && 1 << i <= kPrefillParts && steps > kPrefillAlone; ++i)
             if (pairs * P.kv_heads <= dev.clusters[i]) P.parts = 1 << i;
         // a launch of up to two CTAs a multiprocessor starts while the first
-        // kernel runs (9 ragged requests: 65 us, not 71); a larger one is
-        // slower that way (a prompt of 8192 tokens: 554 us, not 543)
+        // kernel runs (9 ragged requests: 61 us, not 62); a larger one is
+        // slower that way (a prompt of 8192 tokens: 557 us, not 547)
         P.early = pairs && pairs * P.kv_heads * P.parts <= 2 * dev.sms;
     }
     if (c.head_dim == 128) launch_split<128>(P, dev.sms, s);

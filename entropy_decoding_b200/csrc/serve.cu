@@ -7,7 +7,6 @@
 #include <climits>
 #include <cstdint>
 
-#include "check.cuh"
 #include "df11.h"
 #include "serve.h"
 
@@ -30,7 +29,7 @@ __device__ __forceinline__ void flag(int *err, uint32_t bits) {
 // thread reads what another writes.  Pages are those that the table has room
 // for; where rows are cut off at max_tokens, the first CTA writes the pages
 // that they would have started, so every page taken is in the table.  Bound by the launch and two rounds through
-// L2: 3.1 us for 128 requests of a token each, 4.9 us for 509 with up to 2048
+// L2: 3.1 us for 128 requests of a token each, 4.8 us for 509 with up to 2048
 // new tokens each.
 constexpr int kExtendThreads = 512;
 
@@ -156,6 +155,13 @@ __global__ void __launch_bounds__(kExtendThreads) kv_extend_kernel(const df11_kv
 // factors once, took 39 to 45 us for 2 to 5 heads in flight, and 2.3 for 16.
 constexpr int kRopeThreads = 128;
 constexpr int kRopeBatch = 5;  // heads whose loads a thread has in flight
+// CTAs (token, group of heads) up to which a token's heads are shared out: some 7
+// for each of a B200's 148 multiprocessors, about what is resident at a time.
+// Shared out and not, FP32 with norm: 32 + 8 heads of 128 (5 groups) 16 tokens 2.1
+// and 3.5 us, 200 tokens 3.9 and 4.1, 250 4.1 and 4.1, 300 4.8 and 4.3; of 64 (3
+// groups) 200 tokens 2.6 and 2.9, 300 3.5 and 3.1; 16 + 8 heads of 256 (6 groups)
+// 150 tokens 3.8 and 4.6, 200 4.2 and 4.7, 300 5.3 and 4.9.
+constexpr int kRopeGroupedCtas = 7 * 148;
 
 // Four elements as they lie in memory, and as floats.
 template <bool FP32>
@@ -314,10 +320,9 @@ LaunchStatus launch_qk_norm_rope(const df11_qk_norm_rope_args &args, cudaStream_
     const int heads = a.q.n_heads + a.k.n_heads, per = kRopeThreads / (a.head_dim / 8);
     // few tokens: a CTA per token and group of heads, so that every element
     // has its own thread at once; many: one CTA per token, which makes the
-    // angles once for all heads (32 + 8 heads of 128: 200 tokens 3.9 us in
-    // groups and 4.2 without, 300 tokens 4.8 and 4.3)
+    // angles once for all heads
     const int groups = (heads + per - 1) / per;
-    const dim3 grid(a.n_tokens, static_cast<int64_t>(a.n_tokens) * groups <= 7 * 148 ? groups : 1);
+    const dim3 grid(a.n_tokens, static_cast<int64_t>(a.n_tokens) * groups <= kRopeGroupedCtas ? groups : 1);
     switch (a.head_dim) {
         case 64: launch_rope<64>(a, grid, s); break;
         case 128: launch_rope<128>(a, grid, s); break;

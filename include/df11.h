@@ -637,7 +637,8 @@ df11_status df11_rans_decode_launch_shape(const df11_rans_group *g, int *grid, i
  *   df11_kv_extend      the step's pages, slots and positions
  *   df11_decode_gemm    q, k, v = x Wq, x Wk, x Wv (FP32)
  *   df11_qk_norm_rope   norm and rotation of q and k (FP32 -> BF16)
- *   df11_kv4_append     k, v into the cache, 4 bits an element
+ *   df11_kv4_append     k, v into the cache, 4 bits an element (one type for
+ *                       both: v goes to BF16 before, by the caller)
  *   df11_kv4_attention  o = softmax(q k^T) v, the cache decoded on the way
  *                       into the tensor cores (BF16: x of the next GEMM)
  * All are asynchronous on `stream`, allocate nothing, never synchronise, and
@@ -716,7 +717,8 @@ typedef struct {
  * rows of both sides, one launch: y = x / sqrt(mean(x^2) + eps) * weight over
  * a head's head_dim elements (left out when weight is NULL), then each pair
  * (a, b) -> (a cos - b sin, b cos + a sin), the angle position * inv_freq in
- * 64 bits; FP32 throughout, rounded to BF16 once.
+ * 64 bits; FP32 throughout (sum(x^2) too, which passes FP32 where a head has
+ * elements of about 10^19), rounded to BF16 once.
  * Errors: DF11_EINVAL (NULL or misaligned pointer or stride, sizes, eps, out at
  * x in another type or at another stride),
  * DF11_EUNSUPPORTED (head_dim), DF11_ECUDA. */
@@ -803,15 +805,17 @@ uint64_t df11_kv4_attention_workspace_bytes(const df11_kv4_cache *cache, const d
 /* o = softmax(scale * q k^T + mask) v over each request's keys in the cache,
  * decoded on chip.  Softmax statistics and sums in FP32; the products run on
  * the tensor cores in FP16 with FP32 sums (keys and values are exact in FP16,
- * each row of q is scaled by a power of two into FP16's range, probabilities
- * are rounded to FP16).  A row that sees no key gets o = 0 and lse = -inf.
- * Rows behind q_start[n_reqs] are left as they were.  What the pages hold
- * past a request's kv_len never reaches an output.  The result does not
- * depend on timing: calls with equal arguments give equal bits.
+ * each row of q is scaled by a power of two into FP16's range and held to 2^-25
+ * of its largest element, probabilities are rounded to FP16).  A row that sees
+ * no key gets o = 0 and lse = -inf.  Rows behind q_start[n_reqs] are left as they
+ * were.  What the pages hold past a request's kv_len never reaches an output.
+ * The result does not depend on timing: calls with equal arguments give equal
+ * bits.
  * DF11_DEV_ERR_PAGES: a block-table entry out of range, or kv_len past
  * max_pages * page_size (those keys are left out).  DF11_DEV_ERR_AUX:
  * q_start descending or past n_tokens, or a request longer than max_q_len
- * (those rows are not written).
+ * (those rows are not written).  With n_reqs, n_tokens or max_q_len 0 nothing is
+ * launched, and so nothing flagged.
  * Errors: DF11_EINVAL, DF11_EUNSUPPORTED (head_dim, page_size, or a call too
  * large for 31-bit counts, which has to be split: n_tokens * n_q_heads,
  * or the product of n_reqs, n_heads, tiles of 8 of a request's first 64 rows,
