@@ -965,6 +965,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1) attention_split_kernel(const
 // one another.  The decode is hidden (536 us without its conversions).
 constexpr int kPrefillThreads = 512;
 constexpr int kPrefillTile = 128;  // rows of a tile, keys of a step
+// Registers of a thread of the 8 softmax, the 4 decode and the last 4 warps.  More
+// than the block was launched with would be waited for without end.
+constexpr int kSoftmaxRegs = 184, kDecodeRegs = 104, kMmaRegs = 40;
+constexpr int kPrefillRegs = 32 * (8 * kSoftmaxRegs + 4 * kDecodeRegs + 4 * kMmaRegs);
 constexpr int kPrefillParts = 8;   // CTAs of a cluster that share a pair's keys, at most
 // Steps of a pair that one CTA takes alone: a join takes as long as 3 (D = 64)
 // to 5 (D = 128) steps, most of it the transfer between the CTAs' shared memories.
@@ -1307,7 +1311,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
 
     if (warp < 8) {
         // =============================== softmax of tile x, a thread per row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int x = warp >> 2, r = tid & 127;
         const int row = W.row0 + x * kPrefillTile + r;
         const bool live = row < W.rows;
@@ -1537,7 +1541,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
         tc_fence_before();
     } else if (warp < 12) {
         // =============================== the cache to FP16 operand tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecodeRegs));
         constexpr uint32_t NB = D / 16;
         const int u = tid - 256;  // K: the step's key; V: 8 keys and 16 elements
         const int unit = u >> 3;  // V: 16 chunks of 8 keys x NB blocks, lanes of 8 over the chunks of one 128-byte row
@@ -1672,7 +1676,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) attention_prefill_kernel(c
         }
     } else {
         // =============================== MMAs
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
         // one elected lane walks: the instructions between a wait and the MMAs it
         // holds back are on the critical path, so descriptors are made once and
         // the steps go in pairs, whose stages are then constants
@@ -1862,6 +1866,15 @@ bool prepare(Device *d) {
             !allow(&attention_prefill_kernel<64, true>, kPrefillSmem<64>) ||
             !allow(&attention_prefill_kernel<128, false>, kPrefillSmem<128>) ||
             !allow(&attention_prefill_kernel<128, true>, kPrefillSmem<128>))
+            return false;
+        // a build with fewer registers a thread than the roles share out is not launched
+        auto holds = [](auto *kernel) {
+            cudaFuncAttributes f{};
+            return cudaFuncGetAttributes(&f, reinterpret_cast<const void *>(kernel)) == cudaSuccess &&
+                   f.numRegs * kPrefillThreads >= kPrefillRegs;
+        };
+        if (!holds(&attention_prefill_kernel<64, false>) || !holds(&attention_prefill_kernel<64, true>) ||
+            !holds(&attention_prefill_kernel<128, false>) || !holds(&attention_prefill_kernel<128, true>))
             return false;
         for (int i = 1; 1 << i <= kPrefillParts; ++i) known[dev].clusters[i] = max_clusters(1 << i);
         known[dev].sms = std::min(v, kMaxCtas);
